@@ -9,7 +9,7 @@ attention   per sequence b and key/value head g (rep query heads share it): ever
             k = RNE((s - max s) f), f = scale log2(e) 2^(eQ + eK + 6);  E = RNE(2^14 2^(k / 64));
             O = FIT(E AV / sum E), the quotient exact.  The backward pass recomputes E.
 layer norm  rows aligned to one exponent; mean and variance from exact integer sums; the
-            normalised value is an integer multiple of 2^-9.
+            normalised value is an integer multiple of 2^-8.
 FIT(group)  the smallest exponent at which every member rounds (half to even) into +-127.
 
 ``run`` computes this with elementary torch operations where ``own`` is false and with the
@@ -320,7 +320,7 @@ def _norm_rows(st):
     D = (N * s2 - s1 * s1 + torch.where(zero, 0, eps)).float()
     R = torch.where(D > 0, 1 / D.sqrt(), 0)
     u = N * a - s1
-    return u, R, (u * (R.double() * 512)).round(), e
+    return u, R, (u * (R.double() * 256)).round(), e
 
 
 def _vector(t, G, N):
@@ -332,7 +332,7 @@ def _norm_plain_fwd(st):
     N, G = c["cols"], c["G"]
     _, _, h, _ = _norm_rows(st)
     (g, eg), (b, eb) = _vector(st["gamma"], G, N), _vector(st["beta"], G, N)
-    y = (g * torch.exp2(eg - 9) * h + b * torch.exp2(eb)).float()
+    y = (g * torch.exp2(eg - 8) * h + b * torch.exp2(eb)).float()
     return [_fit_values(y.double(), G).to(torch.bfloat16)]
 
 
@@ -346,11 +346,11 @@ def _norm_plain_bwd(st):
     g = (ga * dy).double()
     m1 = (4 * g.sum(1, keepdim=True) / N).round()
     m2 = ((g * h).sum(1, keepdim=True) / N).float().double()
-    t = 4 * g - m1 - (h * m2 * 2.0 ** -16).round()
+    t = 4 * g - m1 - (h * m2 * 2.0 ** -14).round()
     v = t.float() * (R * N)
     dX = _fit_values(v.double() * torch.exp2(eg.double() + edr.double() - e - 2), G)
     dc, ec = _align(Cd, ed, (0,))
-    dg = (dc.double() * h).sum(0, keepdim=True) * torch.exp2(ec.double() - 9)
+    dg = (dc.double() * h).sum(0, keepdim=True) * torch.exp2(ec.double() - 8)
     db = dc.double().sum(0, keepdim=True) * torch.exp2(ec.double())
     return [x.to(torch.bfloat16) for x in (dX, _fit_values(dg, G), _fit_values(db, G))]
 
@@ -553,23 +553,23 @@ def _exact_norm(case, seed):
         if (e[i] != E_ZERO).any():
             D += int(math.floor(EPS[0] * N * N * 2.0 ** (-EPS[1] - 2 * e1)))
         R = f32(1) / np.sqrt(f32(D)) if D else f32(0)
-        h = np.rint((N * a - s1) * (float(R) * 512))
+        h = np.rint((N * a - s1) * (float(R) * 256))
         H[i] = h
         if not back:
-            out[i] = (gv * h / 512 + bv).astype(f32)
+            out[i] = (gv * h / 256 + bv).astype(f32)
             continue
         dy, e2 = _np_align(Cd[i: i + 1], ed[i: i + 1])
         g = (ga[0] * dy[0]).astype(np.int64)
         m1 = np.rint(4 * int(g.sum()) / N)
         m2 = float(f32(int((g * h.astype(np.int64)).sum()) / N))
-        t = 4 * g - m1 - np.rint(h * m2 / 65536)
+        t = 4 * g - m1 - np.rint(h * m2 / 16384)
         out[i] = (t.astype(f32) * (R * f32(N))).astype(np.float64) * 2.0 ** (top + e2 - e1 - 2)
     if not back:
         return [_np_fit(out, G)]
     dg, db = np.zeros((1, N)), np.zeros((1, N))
     for j in range(0, N, G):
         dy, e2 = _np_align(Cd[:, j: j + G], ed[:, j: j + G])
-        dg[0, j: j + G] = (dy * H[:, j: j + G]).sum(0) * 2.0 ** (e2 - 9)
+        dg[0, j: j + G] = (dy * H[:, j: j + G]).sum(0) * 2.0 ** (e2 - 8)
         db[0, j: j + G] = dy.sum(0) * 2.0 ** e2
     return [_np_fit(out, G), _np_fit(dg, G), _np_fit(db, G)]
 
