@@ -403,6 +403,82 @@ int32_t ict_softmax_ce(const ict_tensor *Z, const int32_t *target, int32_t *loss
                        void *stream);
 
 /* --------------------------------------------------------------------------------- */
+/* Layer norm over the columns of each row (Abstract: vision transformers are trained;   */
+/* the pages print no formula for an integer layer norm, so this is a reading).          */
+/*   a = ALIGN_MAX(row of X), e its exponent; S1 = sum a; S2 = sum a^2; u = N a - S1;     */
+/*   D = N S2 - S1^2 + min(floor(eps_mul N^2 2^(-eps_shift - 2 e)), 2^60)  (eps in X's    */
+/*       units as a multiply-shift; no eps term for a row of zeros);                      */
+/*   R = rn24(1 / rn24(sqrt(rn24(D)))), rn24 = rounded to 24 significant bits, R = 0 when  */
+/*       D = 0;   h = RNE(u R 2^8): the normalised row as a 16-bit integer at 2^-8.        */
+/* fwd: Y = FIT(rn24(gamma h 2^-8 + beta)) into Y's groups.  Entries of gamma and beta     */
+/*   whose exponent lies more than 100 below the largest of both count as zero.  beta may  */
+/*   be NULL.                                                                              */
+/* bwd: g = A(gamma) A(dY) (gamma aligned to one exponent, each row of dY to one);         */
+/*   m1 = RNE(4 sum(g) / N), m2 = rn24(rn53(sum(g h) / N)), t = 4 g - m1 - RNE(h m2 2^-14);*/
+/*   dX = FIT(rn24(t rn24(R N)));  dgamma = FIT(sum over rows of A(dY) h 2^-8) and          */
+/*   dbeta = FIT(sum over rows of A(dY)), A here per column group over the rows, the sums   */
+/*   exact.  dbeta may be NULL.  h is recomputed from X: no statistics are kept.           */
+/* X, dY, Y, dX: [rows][N], row-local groups of any widths; gamma, beta, dgamma, dbeta:     */
+/* [1][N].  N and all group widths (below N) multiples of 16, N <= 8192 (ICT_ERR_LAYOUT);   */
+/* pointers and ld 16-byte aligned.  0 <= eps_mul <= 512, 0 <= eps_shift <= 64.             */
+int32_t ict_layernorm_fwd(const ict_tensor *X, const ict_tensor *gamma, const ict_tensor *beta,
+                          int32_t eps_mul, int32_t eps_shift, ict_tensor *Y, void *stream);
+size_t ict_layernorm_bwd_workspace(const ict_tensor *X);
+int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ict_tensor *dY,
+                          int32_t eps_mul, int32_t eps_shift, ict_tensor *dX, ict_tensor *dgamma,
+                          ict_tensor *dbeta, void *ws, size_t ws_bytes, void *stream);
+
+/* --------------------------------------------------------------------------------- */
+/* Attention of `batch` sequences, heads_q query heads sharing heads_kv key/value heads   */
+/* (heads_q a multiple of heads_kv; query head h reads key/value head h / (heads_q /       */
+/* heads_kv)).  Token l of sequence b is row b len_q + l of Q, O, dO, dQ and row b len_k +  */
+/* l of K, V, dK, dV; its head h starts at column q_col + h head_dim (k_col, v_col), at     */
+/* column h head_dim of O and dO.  Q, K and V may be one tensor (the output of one linear  */
+/* layer), dQ, dK and dV likewise.  lens_q, lens_k: device int32 [batch], the valid tokens  */
+/* of each sequence (clamped to [0, len]); NULL means all.  causal = 1: query i sees keys   */
+/* j <= i + lens_k[b] - lens_q[b].  A query that sees no key gives zeros.                   */
+/* Reading (the pages print the softmax table of the output head only), per sequence and    */
+/* key/value head, with every sum exact:                                                    */
+/*   AQ, AK, AV, AdO  the operands aligned (ALIGN_MAX) to one exponent eQ, eK, eV, edO over   */
+/*          the valid tokens and the query heads that share the key/value head               */
+/*   s = AQ AK^T;  k = RNE((s - max s) f), f = rn24(scale_mul 12102203) 2^(-23 - scale_shift  */
+/*       + eQ + eK + 6): logits in 2^-6 of a factor of two (12102203 = log2(e) 2^23);         */
+/*   E = RNE(2^14 2^(k / 64)), the weights in 15 bits (7 bits, as in the head's table, lose   */
+/*       the tail of long rows);  S = sum E;  O = FIT(sum E AV 2^eV / S), the quotient exact. */
+/*   stats  [batch][heads_q][len_q][2]: max s and S (0, 0 for a query that sees no key)       */
+/* Backward, from the forward's O and stats (E is recomputed):                                */
+/*   d = clamp(RNE(sum_d AdO AO 2^(eO - eV)), +-(2^22 - 1)), AO a row of one head aligned;     */
+/*   x = AdO AV^T - d;  X = 127 sum_d |AdO| + |d|;  t = bitlen(X);  T = RNE(E x 2^-t);         */
+/*   dQ = FIT(scale_mul sum_j T AK 2^(-scale_shift + t + edO + eV + eK) / S);                  */
+/*   per block of 128 keys, over the queries that see any of it (all query heads of the       */
+/*   key/value head): p = bitlen(min S) - 1, r = rn24(2^p / rn24(S)), c = max(0, bitlen(max of  */
+/*   floor(r (max_j |T| + 1) 2^t) + X) - 14);  P = RNE(E r);  U = RNE(P x 2^-c);               */
+/*   dV = FIT(sum P AdO 2^(edO - p));  dK = FIT(scale_mul sum U AQ 2^(c - p - scale_shift +     */
+/*   edO + eV + eQ)).                                                                          */
+/* head_dim a multiple of 16 up to 128, heads_q <= 256, batch heads_kv <= 65535, len_q and       */
+/* len_k <= 65536, backward also len_q heads_q / heads_kv <= 65536 (ICT_ERR_LAYOUT); columns,    */
+/* widths and group widths multiples of 16, row-local groups; an output's groups lie inside      */
+/* one head (head_dim and the first column multiples of the group width).  stats 8-byte          */
+/* aligned.  1 <= scale_mul <= 512, 0 <= scale_shift <= 64.                                      */
+typedef struct {
+    int32_t batch, heads_q, heads_kv, len_q, len_k, head_dim, causal, scale_mul, scale_shift;
+    int32_t q_col, k_col, v_col;
+} ict_attn_desc;
+size_t ict_attention_workspace(int32_t backward, const ict_attn_desc *d);
+int32_t ict_attention_fwd(const ict_attn_desc *d, const ict_tensor *Q, const ict_tensor *K,
+                          const ict_tensor *V, const int32_t *lens_q, const int32_t *lens_k,
+                          ict_tensor *O, int32_t *stats, void *ws, size_t ws_bytes, void *stream);
+int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict_tensor *K,
+                          const ict_tensor *V, const int32_t *lens_q, const int32_t *lens_k,
+                          const ict_tensor *O, const ict_tensor *dO, const int32_t *stats,
+                          ict_tensor *dQ, ict_tensor *dK, ict_tensor *dV, void *ws,
+                          size_t ws_bytes, void *stream);
+
+/* The values C 2^e of a tensor as fp32 (bf16 = 0) or bf16 (bf16 = 1) [rows][ld_out] (exact   */
+/* where the type's exponent range holds them).  Any geometry; one pass.                        */
+int32_t ict_values(const ict_tensor *t, int32_t bf16, void *out, int64_t ld_out, void *stream);
+
+/* --------------------------------------------------------------------------------- */
 /* ReLU / ReLU6, the Clip primitive (Table 6: "ReLU / ReLU6 -> Clip"; Table 7): integer  */
 /* operations on the mantissas C, the exponent carried through unchanged.              */
 /*   six = 0: ReLU    forward  Z = max(C, 0)          backward dX = dY * 1[C > 0]       */

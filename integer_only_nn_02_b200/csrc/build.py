@@ -10,12 +10,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 PKG = os.path.dirname(HERE)
 LIB = os.path.join(PKG, "libict.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
-SOURCES = ["ict_api.cu"]
+SOURCES = ["ict_api.cu", "ict_attention.cu", "ict_norm.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "-Xptxas", "-warn-spills",
 ]
 
@@ -36,15 +36,29 @@ def stale() -> bool:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Compiles the sources at the same time, one object each, and links them."""
     if not force and not stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, "-o", tmp] + [os.path.join(HERE, f) for f in SOURCES]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-        print(" ".join(cmd))
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    objs = [f"{tmp}.{i}.o" for i in range(len(SOURCES))]
+    cmds = [[NVCC, *FLAGS, *(["-Xptxas=-v"] if verbose else []), "-c", "-o", o, os.path.join(HERE, f)]
+            for o, f in zip(objs, SOURCES)]
+    try:
+        procs = []
+        for cmd in cmds:
+            if verbose:
+                print(" ".join(cmd))
+            procs.append(subprocess.Popen(cmd))
+        codes = [p.wait() for p in procs]
+        for cmd, code in zip(cmds, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.run([NVCC, *FLAGS, "-shared", "-o", tmp, *objs], check=True)
+        os.replace(tmp, LIB)
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     return LIB
 
 

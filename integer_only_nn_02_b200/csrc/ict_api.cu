@@ -7,11 +7,13 @@
 
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include "ict_device.cuh"
 #include "ict_elementwise.cuh"
 #include "ict_gemm.cuh"
+#include "ict_host.h"
 #include "ict_lut.cuh"
 #include "ict_pointwise.cuh"
 
@@ -1852,6 +1854,8 @@ int32_t ict_get_device_status(int32_t *host_out, void *stream) {
     int32_t v = 0, zero = 0;
     if (cudaMemcpyFromSymbol(&v, g_status, sizeof(v)) != cudaSuccess) return ICT_ERR_CUDA;
     if (cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) != cudaSuccess) return ICT_ERR_CUDA;
+    int st;
+    if ((st = host::take_status_attention(&v)) || (st = host::take_status_norm(&v))) return st;
     if (host_out) *host_out = v;
     if (v & (1 << ICT_ERR_DEVICE_TIMEOUT)) return ICT_ERR_DEVICE_TIMEOUT;
     if (v & (1 << ICT_ERR_EXP_RANGE)) return ICT_ERR_EXP_RANGE;
@@ -2580,3 +2584,31 @@ int32_t ict_avgpool_bwd(const ict_tensor *dY, int32_t n, int32_t h, int32_t w, i
 }
 
 }  // extern "C"
+
+// ---- what the library's other source files share with this one (ict_host.h)
+
+namespace ict {
+namespace host {
+
+int device_info(int *sms) { return ::device_info(sms); }
+int int8_only() { return ::int8_only(); }
+int launch_status() { return ::launch_status(); }
+void counted(int n) { ::counted(n); }
+int check_tensor(const ict_tensor *t) { return ::check_tensor(t); }
+int check_vec(const ict_tensor *t) { return ::check_vec(t); }
+int tmap_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+            uint32_t box_outer, CUtensorMapSwizzle sw) {
+    return ::tmap_2d(m, base, inner, outer, stride, box_inner, box_outer, sw);
+}
+void wait_limits(uint64_t *wait_ns, uint64_t *drain_ns) {
+    std::lock_guard<std::mutex> lk(g_mu);
+    *wait_ns = g_wait_ns;
+    *drain_ns = kDrainNs;
+}
+Timer::Timer(cudaStream_t s, int kernel_class, double work) : impl(new (mem) KTimer(s, kernel_class, work)) {
+    static_assert(sizeof(KTimer) <= sizeof(mem) && alignof(KTimer) <= 8, "room for the timer");
+}
+Timer::~Timer() { static_cast<KTimer *>(impl)->~KTimer(); }
+
+}  // namespace host
+}  // namespace ict

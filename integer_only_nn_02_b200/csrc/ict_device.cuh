@@ -21,8 +21,9 @@ namespace ict {
 constexpr int kEZero = ICT_E_ZERO;
 constexpr int kNoExp = -0x40000000;  // running max of need() before any nonzero member
 
-// Sticky device status word: bit k set <=> status code k was raised on the device.
-__device__ int32_t g_status;
+// Sticky device status word: bit k set <=> status code k was raised on the device.  Every
+// source file of the library has its own; ict_get_device_status() reads them all.
+static __device__ int32_t g_status;
 
 __device__ __forceinline__ void raise_status(int code) { atomicOr(&g_status, 1 << code); }
 
@@ -166,6 +167,74 @@ __device__ __forceinline__ uint32_t pack4s(int a, int b, int c, int d) {
 __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
     return (uint32_t)(a & 0xff) | ((uint32_t)(b & 0xff) << 8) | ((uint32_t)(c & 0xff) << 16) |
            ((uint32_t)(d & 0xff) << 24);
+}
+
+// RNE(C / 2^d) of 16 signed int8 mantissas (|C| <= 127), d >= 0; d >= 8 gives 0.  One
+// half-precision FMA rounds two bytes at once:
+//   h = 1024 + (C + 128)                     (fp16 bits 0x64uu, uu = C ^ 0x80)
+//   h * 2^-d + (1536 - 2^(10-d) - 2^(7-d)) = 1536 + C * 2^-d
+// The three operands are exact in fp16 and the fused multiply-add rounds once.  Its
+// result lies in [1024, 2048), where fp16 integers are spaced by 1, so the rounding is
+// to the nearest integer with ties to even, and the low byte of the result's bits
+// (1536 is 0x6600) is RNE(C / 2^d) in two's complement; d = 0 is exact (1536 + C).  Per
+// four bytes: one XOR, two byte permutes to build the halves, two f16x2 FMAs, one
+// permute to pack, and no branches, so lanes with different shifts stay together.
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+// The FMA's two constants for a shift d in [0, 7], and for index 8 (a shift of 8 or
+// more, or a zero group): multiplier 0 and addend 1536, which leaves every byte 0.
+struct RneK {
+    uint32_t sc, k;  // 2^-d and 1536 - 2^(10-d) - 2^(7-d) in both fp16 halves
+};
+__device__ __forceinline__ RneK rne_consts(int d) {
+    if (d >= 8) return RneK{0u, 0x66006600u};
+    const uint32_t kk = 1536u - (1024u >> d) - (128u >> d);  // an integer in [384, 1527]
+    const uint32_t kb = kk >= 1024u ? kk + 0x6000u : (kk >= 512u ? 2u * kk + 0x5C00u : 4u * kk + 0x5800u);
+    return RneK{(uint32_t)(15 - d) * 0x04000400u, kb * 0x10001u};
+}
+// Kernels that round many vectors keep the nine constant pairs in shared memory.
+__device__ __forceinline__ void rne_table_init(RneK *t) {
+    if (threadIdx.x < 9) t[threadIdx.x] = rne_consts(threadIdx.x);
+}
+// Table index of a vector with group exponent eg aligned to es: the shift, 8 for 8 or
+// more and for a zero group.  A target below eg (never asked for) also maps to 8.
+__device__ __forceinline__ int rne_index(int es, int eg) {
+    return eg == kEZero ? 8 : (int)min((unsigned)(es - eg), 8u);
+}
+__device__ __forceinline__ uint4 rne_shift16_k(uint4 raw, RneK c) {
+    const uint32_t src[4] = {raw.x ^ 0x80808080u, raw.y ^ 0x80808080u, raw.z ^ 0x80808080u, raw.w ^ 0x80808080u};
+    uint32_t o[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = fma_f16x2(__byte_perm(src[q], 0x64646464u, 0x4140), c.sc, c.k);  // bytes 0, 1
+        const uint32_t hi = fma_f16x2(__byte_perm(src[q], 0x64646464u, 0x4342), c.sc, c.k);  // bytes 2, 3
+        o[q] = __byte_perm(lo, hi, 0x6420);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 rne_shift16(uint4 raw, int d) { return rne_shift16_k(raw, rne_consts(d)); }
+
+__device__ __forceinline__ float sx8f(uint32_t w_biased, int b) {
+    // byte b of w (stored with 0x80 added to every byte) as the float C: 2^23 + (C + 128) - (2^23 + 128)
+    return __uint_as_float(__byte_perm(w_biased, 0x4B000000u, 0x7650 | b)) - 8388736.0f;
+}
+__device__ __forceinline__ float pow2f(int k) {  // 2^k for -126 <= k <= 127; 0 below
+    return k < -126 ? 0.0f : __int_as_float((k + 127) << 23);
+}
+__device__ __forceinline__ uint32_t low_bytes4(float a, float b, float c, float d) {
+    return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040),
+                       __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
+}
+// need() of a positive normal float x (its bit pattern): the least S with
+// RNE(x 2^-S) <= 2^(B-1) - 1, i.e. x < (2^(B-1) - 1/2) 2^S: S = E - (B - 2) for
+// x = 1.f 2^E, plus one when 1.f >= 2 - 2^(1-B) (the significand field at or above
+// 2^23 - 2^(24-B)).  A value rounded to odd at 24 bits gives the same S as the exact one,
+// since the bound has at most B significant bits.
+__device__ __forceinline__ int need_rel_f32(uint32_t xb, int qb) {
+    return (int)(xb >> 23) - 127 - (qb - 2) + ((xb & 0x7FFFFFu) >= 0x800000u - (1u << (24 - qb)) ? 1 : 0);
 }
 
 // ------------------------------------------------------------------ warp reductions

@@ -1,0 +1,43 @@
+// ict_host.h -- host-side services of ict_api.cu that the library's other source files use.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/ict.h"
+
+namespace ict {
+namespace host {
+
+int device_info(int *sms);  // ICT_OK on sm_100, and its SM count
+int int8_only();            // ICT_ERR_LAYOUT while the mantissa width is not 8
+int launch_status();
+void counted(int n);        // n kernels launched
+int check_tensor(const ict_tensor *t);
+int check_vec(const ict_tensor *t);  // 16-byte vectors: pointer, ld, cols, group width
+int tmap_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
+            uint32_t box_outer, CUtensorMapSwizzle sw);
+void wait_limits(uint64_t *wait_ns, uint64_t *drain_ns);
+
+// the source files' device status words, OR-ed into *v and cleared (the stream is idle)
+int take_status_attention(int32_t *v);
+int take_status_norm(int32_t *v);
+
+// brackets the launches made during its lifetime with a pair of events (ict_timing_enable)
+struct Timer {
+    Timer(cudaStream_t s, int kernel_class, double work);
+    ~Timer();
+    Timer(const Timer &) = delete;
+    Timer &operator=(const Timer &) = delete;
+
+private:
+    alignas(8) unsigned char mem[48];
+    void *impl;
+};
+
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+}  // namespace host
+}  // namespace ict

@@ -11,6 +11,7 @@ and then make exactly one library call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -51,6 +52,11 @@ class ict_sgd_params(ctypes.Structure):
 
 class ict_conv_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n", "h", "w", "c", "k", "r", "s", "stride", "pad")]
+
+
+class ict_attn_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads_q", "heads_kv", "len_q", "len_k", "head_dim", "causal",
+                                              "scale_mul", "scale_shift", "q_col", "k_col", "v_col")]
 
 
 _P = ctypes.POINTER
@@ -103,6 +109,15 @@ _SIGS = {
     "ict_get_mantissa_bits": ([], _i32),
     "ict_gelu_lut_fwd": ([_P(ict_tensor), _P(ict_tensor), _vp], _i32),
     "ict_gelu_lut_bwd": ([_P(ict_tensor)] * 3 + [_vp], _i32),
+    "ict_layernorm_fwd": ([_P(ict_tensor)] * 3 + [_i32, _i32, _P(ict_tensor), _vp], _i32),
+    "ict_layernorm_bwd_workspace": ([_P(ict_tensor)], _sz),
+    "ict_layernorm_bwd": ([_P(ict_tensor)] * 3 + [_i32, _i32] + [_P(ict_tensor)] * 3 + [_vp, _sz, _vp], _i32),
+    "ict_attention_workspace": ([_i32, _P(ict_attn_desc)], _sz),
+    "ict_attention_fwd": ([_P(ict_attn_desc)] + [_P(ict_tensor)] * 3 + [_vp, _vp, _P(ict_tensor), _vp, _vp, _sz, _vp],
+                          _i32),
+    "ict_attention_bwd": ([_P(ict_attn_desc)] + [_P(ict_tensor)] * 3 + [_vp, _vp] + [_P(ict_tensor)] * 2 + [_vp]
+                          + [_P(ict_tensor)] * 3 + [_vp, _sz, _vp], _i32),
+    "ict_values": ([_P(ict_tensor), _i32, _vp, _i64, _vp], _i32),
     "ict_softmax_ce": ([_P(ict_tensor), _vp, _vp, _P(ict_tensor), _vp], _i32),
 }
 for _name, (_args, _res) in _SIGS.items():
@@ -400,6 +415,79 @@ def ict_softmax_ce(Z: DevCE, target: torch.Tensor, loss: torch.Tensor, dZ: DevCE
            "ict_softmax_ce")
 
 
+def _ref(t: DevCE | None):
+    if t is None:
+        return None
+    if t.mant.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.mant.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return ctypes.byref(t.c())
+
+
+def ict_layernorm_fwd(X: DevCE, gamma: DevCE, beta: DevCE | None, eps, Y: DevCE, stream=None):
+    """eps = (mul, shift): the variance's epsilon mul 2^-shift."""
+    _check(lib.ict_layernorm_fwd(_ref(X), _ref(gamma), _ref(beta), int(eps[0]), int(eps[1]), _ref(Y), _stream(stream)),
+           "ict_layernorm_fwd")
+
+
+def ict_layernorm_bwd_workspace(X: DevCE) -> int:
+    return int(lib.ict_layernorm_bwd_workspace(_ref(X)))
+
+
+def ict_layernorm_bwd(X: DevCE, gamma: DevCE, dY: DevCE, eps, dX: DevCE, dgamma: DevCE, dbeta: DevCE | None, ws=None,
+                      stream=None):
+    nbytes = 0 if ws is None else ws.numel()
+    _check(lib.ict_layernorm_bwd(_ref(X), _ref(gamma), _ref(dY), int(eps[0]), int(eps[1]), _ref(dX), _ref(dgamma),
+                                 _ref(dbeta), _ptr(ws), nbytes, _stream(stream)), "ict_layernorm_bwd")
+
+
+def attn_desc(d: dict) -> ict_attn_desc:
+    """d: batch, heads_q, heads_kv, len_q, len_k, head_dim; causal (False), scale (mul, shift) of mul 2^-shift,
+    and the first columns q_col, k_col, v_col of the heads in Q, K and V (0)."""
+    mul, shift = d["scale"]
+    return ict_attn_desc(*[int(d[k]) for k in ("batch", "heads_q", "heads_kv", "len_q", "len_k", "head_dim")],
+                         int(d.get("causal", False)), int(mul), int(shift),
+                         *[int(d.get(k, 0)) for k in ("q_col", "k_col", "v_col")])
+
+
+def _lens(t: torch.Tensor | None, batch: int):
+    if t is not None:
+        assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch
+    return _ptr(t)
+
+
+def ict_attention_workspace(backward: bool, d: dict) -> int:
+    return int(lib.ict_attention_workspace(int(backward), ctypes.byref(attn_desc(d))))
+
+
+def _stats(t: torch.Tensor, d: dict):
+    assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous()
+    assert t.numel() == 2 * d["batch"] * d["heads_q"] * d["len_q"]
+    return _ptr(t)
+
+
+def ict_attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE, stats: torch.Tensor, ws=None,
+                      stream=None):
+    nbytes = 0 if ws is None else ws.numel()
+    _check(lib.ict_attention_fwd(ctypes.byref(attn_desc(d)), _ref(Q), _ref(K), _ref(V), _lens(lens_q, d["batch"]),
+                                 _lens(lens_k, d["batch"]), _ref(O), _stats(stats, d), _ptr(ws), nbytes,
+                                 _stream(stream)), "ict_attention_fwd")
+
+
+def ict_attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE, dO: DevCE, stats: torch.Tensor,
+                      dQ: DevCE, dK: DevCE, dV: DevCE, ws=None, stream=None):
+    nbytes = 0 if ws is None else ws.numel()
+    _check(lib.ict_attention_bwd(ctypes.byref(attn_desc(d)), _ref(Q), _ref(K), _ref(V), _lens(lens_q, d["batch"]),
+                                 _lens(lens_k, d["batch"]), _ref(O), _ref(dO), _stats(stats, d), _ref(dQ), _ref(dK),
+                                 _ref(dV), _ptr(ws), nbytes, _stream(stream)), "ict_attention_bwd")
+
+
+def ict_values(t: DevCE, out: torch.Tensor, stream=None):
+    bf16 = {torch.float32: 0, torch.bfloat16: 1}[out.dtype]
+    assert out.is_cuda and tuple(out.shape) == (t.rows, t.cols) and (t.cols <= 1 or out.stride(1) == 1)
+    _check(lib.ict_values(_ref(t), bf16, _ptr(out), out.stride(0) if t.rows > 1 else max(t.cols, 1), _stream(stream)),
+           "ict_values")
+
+
 # ----------------------------------------------------------------- conveniences
 
 def ict_relu_fwd(X: DevCE, six: bool, Z: DevCE, stream=None):
@@ -520,6 +608,64 @@ def softmax_ce(Z: DevCE, target: torch.Tensor, g_cols: int | None = None, stream
     dZ = DevCE.empty(Z.rows, Z.cols, 1, g_cols or Z.cols)
     ict_softmax_ce(Z, target.to(device="cuda", dtype=torch.int32), loss, dZ, stream)
     return loss, dZ
+
+
+def _on(stream):
+    """Allocations made inside belong to the stream that the call runs on."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def layernorm_fwd(X: DevCE, gamma: DevCE, beta: DevCE | None = None, eps=(1, 20), g_cols=32, stream=None) -> DevCE:
+    with _on(stream):
+        Y = DevCE.empty(X.rows, X.cols, 1, g_cols, X.mant.device)
+        ict_layernorm_fwd(X, gamma, beta, eps, Y)
+    return Y
+
+
+def layernorm_bwd(X: DevCE, gamma: DevCE, dY: DevCE, eps=(1, 20), g_cols=32, stream=None):
+    """(dX, dgamma, dbeta), all in (1, g_cols) groups."""
+    dev = X.mant.device
+    with _on(stream):
+        dX = DevCE.empty(X.rows, X.cols, 1, g_cols, dev)
+        dg, db = DevCE.empty(1, X.cols, 1, g_cols, dev), DevCE.empty(1, X.cols, 1, g_cols, dev)
+        ict_layernorm_bwd(X, gamma, dY, eps, dX, dg, db, _ws(ict_layernorm_bwd_workspace(X), dev))
+    return dX, dg, db
+
+
+def attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, g_cols=32, lens_q=None, lens_k=None, stream=None):
+    """(O [batch * len_q, heads_q * head_dim] in (1, g_cols) groups, stats for the backward pass).  See attn_desc for d."""
+    dev = Q.mant.device
+    with _on(stream):
+        O = DevCE.empty(d["batch"] * d["len_q"], d["heads_q"] * d["head_dim"], 1, g_cols, dev)
+        stats = torch.empty((d["batch"] * d["heads_q"] * d["len_q"], 2), dtype=torch.int32, device=dev)
+        ict_attention_fwd(d, Q, K, V, lens_q, lens_k, O, stats, _ws(ict_attention_workspace(False, d), dev))
+    return O, stats
+
+
+def attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, O: DevCE, dO: DevCE, stats: torch.Tensor, g_cols=32,
+                  lens_q=None, lens_k=None, stream=None):
+    """(dQ, dK, dV) in (1, g_cols) groups, laid out like Q, K and V: operands that share one tensor share their
+    gradient's tensor (columns of no head stay unwritten)."""
+    made = {}
+
+    def like(t: DevCE) -> DevCE:
+        if id(t) not in made:
+            made[id(t)] = DevCE.empty(t.rows, t.cols, 1, g_cols, t.mant.device)
+        return made[id(t)]
+
+    with _on(stream):
+        dQ, dK, dV = like(Q), like(K), like(V)
+        ict_attention_bwd(d, Q, K, V, lens_q, lens_k, O, dO, stats, dQ, dK, dV,
+                          _ws(ict_attention_workspace(True, d), Q.mant.device))
+    return dQ, dK, dV
+
+
+def values(t: DevCE, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+    """The values C 2^e of t [rows, cols]."""
+    with _on(stream):
+        out = torch.empty((t.rows, t.cols), dtype=dtype, device=t.mant.device)
+        ict_values(t, out)
+    return out
 
 
 def device_status(stream=None) -> int:
