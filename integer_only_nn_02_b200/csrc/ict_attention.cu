@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "ict_attention.cuh"
+#include "ict_attention_fwd.cuh"
 #include "ict_host.h"
 
 namespace ict {
@@ -96,45 +97,6 @@ __device__ __forceinline__ void store_row(const AttnArgs &a, const AttnOut &out,
         }
         if (lane == 0) out.exp[row * out.ngc + col / out.G + g] = (int8_t)e;
     }
-}
-
-// One warp per query row: the largest score, then the weights 32 keys at a time.
-__global__ void __launch_bounds__(128) attn_fwd_simple(const __grid_constant__ AttnArgs a) {
-    __shared__ int sw[4][32];
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int64_t r = (int64_t)blockIdx.x * 4 + wp;
-    if (r >= (int64_t)a.B * a.Hq * a.Lq) return;
-    const int i = (int)(r % a.Lq), bh = (int)(r / a.Lq), h = bh % a.Hq, b = bh / a.Hq, g = h / a.rep;
-    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk);
-    const int see = i >= nq ? 0 : (a.causal ? min(nk, max(0, i + nk - nq + 1)) : nk);
-    const int nv = a.Dp / 16;
-    const uint4 *q = copy_row(a, OPQ, b, h, i);
-    int mx = INT_MIN;
-    for (int j = lane; j < see; j += 32) mx = max(mx, dot_row(q, copy_row(a, OPK, b, g, j), nv));
-    mx = warp_max(mx);
-    const float f = attn_factor(a, b * a.Hkv + g);
-    int S = 0;
-    int64_t acc[4] = {0, 0, 0, 0};
-    for (int j0 = 0; j0 < see; j0 += 32) {
-        int E = 0;
-        if (j0 + lane < see) {
-            const int s = dot_row(q, copy_row(a, OPK, b, g, j0 + lane), nv);
-            E = __float_as_int(attn_weight((float)(s - mx), f)) - 0x4B400000;
-        }
-        S += E;
-        sw[wp][lane] = E;
-        __syncwarp();
-        for (int j = 0; j < 32 && j0 + j < see; ++j) {
-            const int8_t *v = reinterpret_cast<const int8_t *>(copy_row(a, OPV, b, g, j0 + j));
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k * 32 + lane < a.Dp) acc[k] += (int64_t)sw[wp][j] * v[k * 32 + lane];
-        }
-        __syncwarp();
-    }
-    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-    if (lane == 0) a.stats[r] = make_int2(see ? mx : 0, S);
-    store_row(a, a.o, (int64_t)b * a.Lq + i, h, acc, S ? (double)S : 1.0, attn_top(a, OPV, b * a.Hkv + g));
 }
 
 // ------------------------------------------------------------------ backward
@@ -424,6 +386,29 @@ int align_operands(const AttnArgs &a, cudaStream_t s) {
     return host::launch_status();
 }
 
+// [rows][Dp] aligned copy of an operand as boxes of 128 rows and 64 columns
+int copy_map(CUtensorMap *m, const AttnArgs &a, int op) {
+    const AttnOperand &o = a.op[op];
+    return host::tmap_2d(m, o.copy, (uint64_t)a.Dp, (uint64_t)std::max<int64_t>((int64_t)a.B * o.heads * o.L, 1), (uint64_t)a.Dp,
+                         64, 128, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int DP>
+int launch_fwd(const AttnArgs &a, cudaStream_t s) {
+    using L = FwdCfg<DP>;
+    CUtensorMap q, k, v;
+    int st;
+    if ((st = copy_map(&q, a, OPQ)) || (st = copy_map(&k, a, OPK)) || (st = copy_map(&v, a, OPV))) return st;
+    if (cudaFuncSetAttribute(attn_fwd_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
+        return ICT_ERR_CUDA;
+    AttnLimits lim;
+    host::wait_limits(&lim.wait_ns, &lim.drain_ns);
+    const int64_t blocks = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
+    attn_fwd_kernel<DP><<<(unsigned)blocks, L::kThreads, L::kBytes, s>>>(q, k, v, a, lim);
+    host::counted(1);
+    return host::launch_status();
+}
+
 }  // namespace
 
 namespace host {
@@ -462,9 +447,7 @@ int32_t ict_attention_fwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     cudaStream_t s = (cudaStream_t)stream;
     host::Timer kt(s, ICT_KC_GEMM, 4.0 * (double)rows * a.Lk * a.D);
     if ((st = align_operands(a, s))) return st;
-    attn_fwd_simple<<<(unsigned)host::cdiv(rows, 4), 128, 0, s>>>(a);
-    host::counted(1);
-    return host::launch_status();
+    return a.Dp == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
 }
 
 int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict_tensor *K, const ict_tensor *V,

@@ -84,4 +84,86 @@ __device__ __forceinline__ int quot_mant(double q, int S) {  // RNE(q 2^-S), sat
     return v > 127 ? 127 : (v < -127 ? -127 : v);
 }
 
+// ---- pairs of fp32 values: one instruction works on both halves of a 64-bit register
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pk(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pk(float a) { return pk(a, a); }
+__device__ __forceinline__ void unpk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The bit patterns 0x4B400000 + E of two weights from two scores: bias = 0x4B400000 - smax
+// (mod 2^32), so that the integer sum is the float 1.5 2^23 + (s - smax) itself.
+__device__ __forceinline__ void attn_weight2(uint32_t s0, uint32_t s1, uint32_t bias, f2 f64th, float &w0, float &w1) {
+    const f2 n = add2(pk(__uint_as_float(s0 + bias), __uint_as_float(s1 + bias)), pk(-kAttnMagic));
+    const f2 y = add2(fma2(n, f64th, pk(kGridMagic)), pk(-kGridMagic));
+    float a, b;
+    unpk(y, a, b);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    unpk(fma2(pk(a, b), pk(16384.0f), pk(kAttnMagic)), w0, w1);
+}
+// low and second bytes of four words
+__device__ __forceinline__ void split_bytes(float a, float b, float c, float d, uint32_t &lo, uint32_t &hi) {
+    const uint32_t ab = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5140);
+    const uint32_t cd = __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x5140);
+    lo = __byte_perm(ab, cd, 0x5410);
+    hi = __byte_perm(ab, cd, 0x7632);
+}
+// 16-byte chunk c of row r of a [128][128-byte] tile in the 128-byte swizzle
+__device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+// tcgen05.wait::ld after which the loaded registers may be used: the empty statements take
+// them as operands, so that no use is scheduled before the wait
+template <int N>
+__device__ __forceinline__ void tmem_tie(uint32_t (&v)[N]) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) asm volatile("" : "+r"(v[q]));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N]) {
+    tmem_ld_wait();
+    tmem_tie(v);
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N], uint32_t (&w)[N]) {
+    tmem_ld_wait();
+    tmem_tie(v);
+    tmem_tie(w);
+}
+
+// One arrival per warp once all its lanes are here (their TMEM reads waited for): an arrival
+// per thread costs a serial shared-memory atomic each.
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// n 2^-S / den as a mantissa, rden = 2^-S / den rounded: the product is within 2^-45 of the
+// quotient, and a quotient that is not half way between two whole numbers is at least 2^-41
+// away from that (n < 2^47), so adding and taking away 1.5 2^9 (spacing 2^-43) restores
+// exact ties and moves nothing else across one.
+__device__ __forceinline__ int quot_mant_fast(double n, double rden) {
+    const double q = (n * rden + 768.0) - 768.0;
+    return __double2loint(q + 6755399441055744.0);
+}
+
 }  // namespace ict
