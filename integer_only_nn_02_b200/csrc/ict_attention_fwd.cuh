@@ -19,6 +19,8 @@
 // Every wait is bounded as in the Product kernels.
 #pragma once
 
+#include <type_traits>
+
 #include "ict_attention.cuh"
 
 namespace ict {
@@ -30,7 +32,7 @@ template <int DP>
 struct FwdCfg {
     static constexpr int H = DP / 64;          // 64-column halves of a head
     static constexpr int NWG = 2;
-    static constexpr int SB = DP == 64 ? 1 : 2;  // score buffers of pass 2
+    static constexpr int TN = DP == 64 ? 64 : 128;  // keys of a pass 2 step (two score buffers of TN columns)
     static constexpr int KS = DP == 64 ? 3 : 2, VS = 2;
     static constexpr int kTile = H * kHalfTile;
     static constexpr int kOffK = kTile, kOffV = kOffK + KS * kTile;
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ AttnArgs a,
                     const __grid_constant__ AttnLimits lim) {
     using L = FwdCfg<DP>;
-    constexpr int H = L::H, NWG = L::NWG, CW = 128 / NWG, NS = 128 * NWG;
+    // a softmax thread's columns of a 128-key tile (pass 1) and of a TN-key step (pass 2)
+    constexpr int H = L::H, NWG = L::NWG, CW = 128 / NWG, CW2 = L::TN / NWG, NS = 128 * NWG;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(smem);
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
     const uint32_t bar_of = bar_ee + 8, bar_dr = bar_of + 8;           // output complete, drain
     volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);
     volatile int *abort_flag = &misc[1];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     // heavy causal tiles first
     const int ntq = (a.Lq + kQTile - 1) / kQTile, heads = a.B * a.Hq;
@@ -239,7 +242,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm = (uint32_t)misc[0];
+    const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
     auto fail = [&]() {
         *abort_flag = 1;
         raise_status(ICT_ERR_DEVICE_TIMEOUT);
@@ -281,61 +284,79 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
         }
     } else if (warp == 4 * NWG + 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0 && nt > 0) {
-            constexpr uint32_t kIdS = idesc_i8(128, 128);
+        // the whole warp runs this loop, one elected lane issues
+        if (nt > 0) {
             constexpr uint32_t kIdO = idesc_i8(128, DP, false, true) & ~(1u << 7);  // unsigned A
-            bool ok = mbar_wait(bar_q, 0, lim.wait_ns, abort_flag);
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, lim.wait_ns, abort_flag));
+            };
+            bool ok = wait(bar_q, 0);
             int kn = 0, n1[2] = {0, 0};
-            // S of the next K tile into buffer buf; a buffer is free once pass 1 has read it
-            auto scores = [&](int buf, bool read) {
+            // S of N keys from row `half` * N of the next K tile into score buffer buf at column col
+            auto scores = [&](auto n_keys, int buf, int col, int half, bool done) {
+                constexpr int N = decltype(n_keys)::value;
                 const int s = kn % L::KS;
-                if (!mbar_wait(bar_kf + 8 * s, (kn / L::KS) & 1, lim.wait_ns, abort_flag)) return false;
-                if (read && n1[buf] > 0 && !mbar_wait(bar_se + 8 * buf, (n1[buf] - 1) & 1, lim.wait_ns, abort_flag))
-                    return false;
+                if (half == 0 && !wait(bar_kf + 8 * s, (kn / L::KS) & 1)) return false;
                 tc_fence_after();
-                const uint32_t kb = sb + L::kOffK + s * L::kTile;
+                const uint32_t kb = sb + L::kOffK + s * L::kTile + half * N * 64;
+                const uint64_t da = smem_desc_kmajor(sb, 64), db = smem_desc_kmajor(kb, 64);
+                if (elect_one()) {
 #pragma unroll
-                for (int x = 0; x < H; ++x) {
-                    const uint64_t da = smem_desc_kmajor(sb + x * kHalfTile, 64), db = smem_desc_kmajor(kb + x * kHalfTile, 64);
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) umma_i8(tm + buf * 128, da + 2 * kk, db + 2 * kk, kIdS, (x | kk) ? 1u : 0u);
+                    for (int x = 0; x < 2 * H; ++x)
+                        umma_i8(tm + col, da + (x >> 1) * (kHalfTile >> 4) + 2 * (x & 1),
+                                db + (x >> 1) * (kHalfTile >> 4) + 2 * (x & 1), idesc_i8(128, N), x ? 1u : 0u);
+                    if (done) umma_commit(bar_ke + 8 * s);
+                    umma_commit(bar_sf + 8 * buf);
                 }
-                umma_commit(bar_ke + 8 * s);
-                umma_commit(bar_sf + 8 * buf);
-                ++kn;
+                __syncwarp();
+                if (done) ++kn;
                 return true;
             };
+            constexpr auto n128 = std::integral_constant<int, 128>();
+            constexpr auto nTN = std::integral_constant<int, L::TN>();
             for (int t = 0; t < nt && ok; ++t) {
-                ok = scores(t & 1, true);
-                ++n1[t & 1];
+                const int buf = t & 1;  // free once pass 1 has read its last scores
+                ok = (n1[buf] == 0 || wait(bar_se + 8 * buf, (n1[buf] - 1) & 1)) && scores(n128, buf, buf * 128, 0, true);
+                ++n1[buf];
             }
-            if (ok) ok = scores(0, true);
-            for (int t = 0; t < nt && ok; ++t) {
-                if (L::SB == 2 && t + 1 < nt) {  // buffer of the weights t - 1
-                    if (t > 0) ok = mbar_wait(bar_ee, (t - 1) & 1, lim.wait_ns, abort_flag);
-                    if (!ok || !(ok = scores((t + 1) & 1, t == 0))) break;
+            constexpr int PER = 128 / L::TN;  // steps of a K or V tile
+            const int nu = (most + L::TN - 1) / L::TN;
+            // both of pass 2's 64-wide buffers lie in pass 1's first one
+            if (ok) ok = wait(bar_se, (n1[0] - 1) & 1) && scores(nTN, 0, 0, 0, PER == 1 || nu == 1);
+            for (int u = 0; u < nu && ok; ++u) {
+                if (u + 1 < nu) {  // the next scores, in the buffer of the weights u - 1
+                    if (u > 0) ok = wait(bar_ee, (u - 1) & 1);
+                    // before its barrier completes another phase, every warp has seen pass 1's last
+                    else if (n1[1] > 0) ok = wait(bar_se + 8, (n1[1] - 1) & 1);
+                    const int half = (u + 1) % PER;
+                    if (!ok || !(ok = scores(nTN, (u + 1) & 1, ((u + 1) & 1) * L::TN, half, half == PER - 1 || u + 2 == nu))) break;
                 }
-                const int v = t % L::VS;
-                ok = mbar_wait(bar_vf + 8 * v, (t / L::VS) & 1, lim.wait_ns, abort_flag) &&
-                     mbar_wait(bar_ef + 8 * (L::SB == 2 ? t & 1 : 0), (L::SB == 2 ? t >> 1 : t) & 1, lim.wait_ns, abort_flag);
+                const int v = (u / PER) % L::VS;
+                ok = (u % PER != 0 || wait(bar_vf + 8 * v, (u / PER / L::VS) & 1)) && wait(bar_ef + 8 * (u & 1), (u >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                const int ks = (min(128, most - t * 128) + 31) / 32;
-                const uint64_t dv = smem_desc_mnmajor64(sb + L::kOffV + v * L::kTile, kHalfTile);
-                const uint32_t e0 = tm + (L::SB == 2 ? t & 1 : 0) * 128;
+                const int ks = (min(L::TN, most - u * L::TN) + 31) / 32;
+                const uint64_t dv = smem_desc_mnmajor64(sb + L::kOffV + v * L::kTile + (u % PER) * L::TN * 64, kHalfTile);
+                const uint32_t e0 = tm + (u & 1) * L::TN, first = u ? 1u : 0u;
+                if (elect_one()) {
 #pragma unroll
-                for (int pl = 0; pl < 2; ++pl)
-                    for (int kk = 0; kk < ks; ++kk)
-                        umma_i8_ta(tm + L::kO + pl * DP, e0 + (kk >> 1) * 64 + (kk & 1) * 8 + pl * 16, dv + 128 * kk, kIdO,
-                                   (t | kk) ? 1u : 0u);
-                umma_commit(bar_ve + 8 * v);
-                umma_commit(bar_ee);
-                if (L::SB == 1 && t + 1 < nt)  // the weights lie in the only score buffer
-                    ok = mbar_wait(bar_ee, t & 1, lim.wait_ns, abort_flag) && scores(0, false);
+                    for (int kk = 0; kk < L::TN / 32; ++kk)
+                        if (kk < ks) {
+                            const uint32_t e = e0 + kk / (CW2 / 32) * CW2 + kk % (CW2 / 32) * 8;
+                            umma_i8_ta(tm + L::kO, e, dv + 128 * kk, kIdO, kk ? 1u : first);
+                            umma_i8_ta(tm + L::kO + DP, e + CW2 / 4, dv + 128 * kk, kIdO, kk ? 1u : first);
+                        }
+                    if (u % PER == PER - 1 || u + 1 == nu) umma_commit(bar_ve + 8 * v);
+                    umma_commit(bar_ee);
+                }
+                __syncwarp();
             }
-            if (!ok) fail();
-            umma_commit(bar_of);
-            umma_commit(bar_dr);
+            if (!ok && lane == 0) fail();
+            if (elect_one()) {
+                umma_commit(bar_of);
+                umma_commit(bar_dr);
+            }
+            __syncwarp();
             mbar_wait(bar_dr, 0, lim.drain_ns, nullptr);
         }
     } else {
@@ -381,18 +402,19 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
         const f2 f = pk(attn_factor(a, b * a.Hkv + g));
         uint32_t sum = 0;
         int n_sum = 0;
-        for (int t = 0; t < nt && ok; ++t) {
-            const int buf = L::SB == 2 ? t & 1 : 0;
+        const int nu = (most + L::TN - 1) / L::TN;
+        for (int u = 0; u < nu && ok; ++u) {
+            const int buf = u & 1;
             ok = __all_sync(0xffffffffu, mbar_wait(bar_sf + 8 * buf, sn[buf] & 1, lim.wait_ns, abort_flag));
             if (!ok) break;
             ++sn[buf];
             tc_fence_after();
-            const int end = min(128, most - t * 128);  // columns that the MMAs read
+            const int end = min(L::TN, most - u * L::TN);  // columns that the MMAs read
             // the weights' two byte planes take the first half of this thread's own score columns
-            const uint32_t mine = tm + lanes + buf * 128 + wg * CW;
-#pragma unroll 1
-            for (int c = 0; c < CW; c += 32) {
-                const int cc = wg * CW + c, col = t * 128 + cc;
+            const uint32_t mine = tm + lanes + buf * L::TN + wg * CW2;
+#pragma unroll
+            for (int c = 0; c < CW2; c += 32) {
+                const int cc = wg * CW2 + c, col = u * L::TN + cc;
                 if (cc >= end) break;
                 uint32_t lo[8], hi[8];
                 if (col < see_max) {
@@ -407,7 +429,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
                     for (int q = 0; q < 8; ++q) lo[q] = hi[q] = 0;
                 }
                 tmem_st8(mine + c / 4, hi);
-                tmem_st8(mine + 16 + c / 4, lo);
+                tmem_st8(mine + CW2 / 4 + c / 4, lo);
             }
             tmem_st_wait();
             warp_arrive(bar_ef + 8 * buf);
