@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "ict_attention.cuh"
+#include "ict_attention_bwd.cuh"
 #include "ict_attention_fwd.cuh"
 #include "ict_host.h"
 
@@ -58,224 +59,49 @@ __global__ void __launch_bounds__(256) attn_copy_kernel(const __grid_constant__ 
     }
 }
 
-__device__ __forceinline__ int dot_row(const uint4 *x, const uint4 *y, int nv) {
-    int s = 0;
-    for (int v = 0; v < nv; ++v) {
-        const uint4 p = x[v], q = y[v];
-        s = __dp4a((int)p.x, (int)q.x, s);
-        s = __dp4a((int)p.y, (int)q.y, s);
-        s = __dp4a((int)p.z, (int)q.z, s);
-        s = __dp4a((int)p.w, (int)q.w, s);
-    }
-    return s;
-}
-__device__ __forceinline__ const uint4 *copy_row(const AttnArgs &a, int op, int b, int h, int l) {
-    const AttnOperand &o = a.op[op];
-    return reinterpret_cast<const uint4 *>(o.copy + (((int64_t)b * o.heads + h) * o.L + l) * a.Dp);
-}
-
-// A row of D quotients acc / den at exponent r (lane holds columns lane, lane + 32, ...),
-// FIT into groups of out.G columns.  One warp.
-__device__ __forceinline__ void store_row(const AttnArgs &a, const AttnOut &out, int64_t row, int h,
-                                          const int64_t (&acc)[4], double den, int r) {
-    const int lane = threadIdx.x & 31;
-    const int col = out.col + h * a.D;
-    for (int g = 0; g < a.D / out.G; ++g) {
-        double mx = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int d = k * 32 + lane;
-            if (d < a.D && d / out.G == g) mx = fmax(mx, fabs((double)acc[k] / den));
-        }
-        for (int o = 16; o > 0; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int e = mx > 0 ? finalize_exp(need_quot(mx) + r) : kEZero;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int d = k * 32 + lane;
-            if (d < a.D && d / out.G == g)
-                out.mant[row * out.ld + col + d] = mx > 0 ? (int8_t)quot_mant((double)acc[k] / den, e - r) : (int8_t)0;
-        }
-        if (lane == 0) out.exp[row * out.ngc + col / out.G + g] = (int8_t)e;
-    }
-}
-
 // ------------------------------------------------------------------ backward
 
-// delta' = clamp(RNE(sum_d dO O 2^(eO - eV))), X = 127 sum |dO| + |delta'|; one warp per row
+// d = clamp(RNE(sum_d AdO AO 2^(eO - eV))), X = 127 sum |AdO| + |d|: a lane per 16 columns.
+template <int NL>
 __global__ void __launch_bounds__(256) attn_row_kernel(const __grid_constant__ AttnArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (r >= (int64_t)a.B * a.Hq * a.Lq) return;
+    const int v = threadIdx.x % NL;
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Lq, at = (int64_t)blockIdx.x * (256 / NL) + threadIdx.x / NL;
+    const int64_t r = min(at, rows - 1);
     const int i = (int)(r % a.Lq), bh = (int)(r / a.Lq), h = bh % a.Hq, b = bh / a.Hq;
-    const bool valid = i < clamp_len(a.op[OPQ].lens, b, a.Lq);
     const int64_t row = (int64_t)b * a.Lq + i;
-    const int v = lane, vec = (h * a.D) / 16 + v;
-    const bool on = v < a.D / 16 && valid;
+    const int vec = (h * a.D) / 16 + v;
+    const bool on = v < a.D / 16 && i < clamp_len(a.op[OPQ].lens, b, a.Lq);
     const int e = on ? a.o_exp[row * a.o_ngc + vec / a.o_gv] : kEZero;
-    const int es = warp_max(e == kEZero ? kNoExp : e);
-    int dot = 0, sum = 0;
+    uint4 w = make_uint4(0, 0, 0, 0), d = w;
     if (on) {
-        const uint4 w = rne_shift16(*reinterpret_cast<const uint4 *>(a.o_mant + row * a.o_ld + vec * 16), rne_index(es, e));
-        const uint4 d = copy_row(a, OPD, b, h, i)[v];
-        const uint32_t o4[4] = {w.x, w.y, w.z, w.w}, d4[4] = {d.x, d.y, d.z, d.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            dot = __dp4a((int)o4[q], (int)d4[q], dot);
-            sum = __dp4a((int)__vabs4(d4[q]), 0x01010101, sum);
-        }
+        w = *reinterpret_cast<const uint4 *>(a.o_mant + row * a.o_ld + (int64_t)vec * 16);
+        d = *reinterpret_cast<const uint4 *>(a.op[OPD].copy + r * a.Dp + v * 16);
     }
-    for (int o = 16; o > 0; o >>= 1) {
+    int es = e == kEZero ? kNoExp : e;
+    for (int o = NL / 2; o > 0; o >>= 1) es = max(es, __shfl_xor_sync(0xffffffffu, es, o));
+    w = rne_shift16(w, rne_index(es, e));
+    const uint32_t o4[4] = {w.x, w.y, w.z, w.w}, d4[4] = {d.x, d.y, d.z, d.w};
+    int dot = 0, sum = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        dot = __dp4a((int)o4[q], (int)d4[q], dot);
+        sum = __dp4a((int)__vabs4(d4[q]), 0x01010101, sum);
+    }
+    for (int o = NL / 2; o > 0; o >>= 1) {
         dot += __shfl_xor_sync(0xffffffffu, dot, o);
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    if (lane == 0) {
+    if (v == 0 && at < rows) {
         const int k = es <= kNoExp ? 0 : es - attn_top(a, OPV, b * a.Hkv + h / a.rep);
         int delta;
         if (k >= 0) {
-            const int64_t w = (int64_t)dot << min(k, 24);  // |dot| < 2^22: beyond 24 only the bound remains
-            delta = (int)max((int64_t)-kDeltaMax, min((int64_t)kDeltaMax, w));
+            const int64_t x = (int64_t)dot << min(k, 24);  // |dot| < 2^22: beyond 24 only the bound remains
+            delta = (int)max((int64_t)-kDeltaMax, min((int64_t)kDeltaMax, x));
         } else {
             delta = rne_shr32(dot, -k);
         }
         a.row[r] = make_int2(delta, 127 * sum + abs(delta));
     }
-}
-
-__device__ __forceinline__ int bitlen32(int x) { return 32 - __clz(x); }
-
-// dQ, one warp per query row
-__global__ void __launch_bounds__(128) attn_dq_simple(const __grid_constant__ AttnArgs a) {
-    __shared__ int sw[4][32];
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int64_t r = (int64_t)blockIdx.x * 4 + wp;
-    if (r >= (int64_t)a.B * a.Hq * a.Lq) return;
-    const int i = (int)(r % a.Lq), bh = (int)(r / a.Lq), h = bh % a.Hq, b = bh / a.Hq, g = h / a.rep;
-    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk);
-    const int see = i >= nq ? 0 : (a.causal ? min(nk, max(0, i + nk - nq + 1)) : nk);
-    const int nv = a.Dp / 16;
-    const uint4 *q = copy_row(a, OPQ, b, h, i), *dd = copy_row(a, OPD, b, h, i);
-    const int2 st = a.stats[r], rw = a.row[r];
-    const int tau = bitlen32(rw.y);
-    const float f = attn_factor(a, b * a.Hkv + g), sc = pow2f(-tau);
-    int64_t acc[4] = {0, 0, 0, 0};
-    int tm = 0;
-    for (int j0 = 0; j0 < see; j0 += 32) {
-        int T = 0;
-        if (j0 + lane < see) {
-            const int s = dot_row(q, copy_row(a, OPK, b, g, j0 + lane), nv);
-            const float E = attn_weight((float)(s - st.x), f) - kAttnMagic;
-            const int x = dot_row(dd, copy_row(a, OPV, b, g, j0 + lane), nv) - rw.x;
-            T = __float_as_int(__fmaf_rn(E * sc, (float)x, kAttnMagic)) - 0x4B400000;
-        }
-        tm = max(tm, abs(T));
-        sw[wp][lane] = T;
-        __syncwarp();
-        for (int j = 0; j < 32 && j0 + j < see; ++j) {
-            const int8_t *v = reinterpret_cast<const int8_t *>(copy_row(a, OPK, b, g, j0 + j));
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k * 32 + lane < a.Dp) acc[k] += (int64_t)sw[wp][j] * v[k * 32 + lane];
-        }
-        __syncwarp();
-    }
-    tm = warp_max(tm);
-    if (lane == 0) a.tmax[r] = tm;
-    const int bg = b * a.Hkv + g;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] *= a.mul;
-    store_row(a, a.o, (int64_t)b * a.Lq + i, h, acc, st.y ? (double)st.y : 1.0,
-              tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift);
-}
-
-// rn24(2^pi / rn24(S)) of a row; 0 for a row that sees no key
-__device__ __forceinline__ float attn_rho(int S, int pi) { return S > 0 ? __fdiv_rn(pow2f(pi), (float)S) : 0.0f; }
-// no |P x| of the row is larger
-__device__ __forceinline__ int64_t attn_bound(float rho, int tmax, int X) {
-    return (int64_t)floor((double)rho * (double)(tmax + 1) * pow2d(bitlen32(X))) + X;
-}
-
-// pi and c of every block of 128 keys: the smallest sum of weights, then the largest bound,
-// over the rows of all the head's queries that see the block.  One block per (b, g, J).
-__global__ void __launch_bounds__(256) attn_block_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ int smin;
-    __shared__ unsigned long long wmax;
-    const int J = blockIdx.x, bg = blockIdx.y, b = bg / a.Hkv, g = bg % a.Hkv;
-    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk);
-    const int j0 = J * kKeyBlock;
-    const int i0 = a.causal ? max(0, j0 - (nk - nq)) : 0;
-    if (threadIdx.x == 0) smin = INT_MAX, wmax = 0;
-    __syncthreads();
-    const int n = j0 < nk ? max(0, nq - i0) : 0, total = n * a.rep;
-    auto index = [&](int t) { return ((int64_t)b * a.Hq + g * a.rep + t / n) * a.Lq + i0 + t % n; };
-    int m = INT_MAX;
-    for (int t = threadIdx.x; t < total; t += 256) {
-        const int S = a.stats[index(t)].y;
-        if (S > 0) m = min(m, S);
-    }
-    m = -warp_max(-m);
-    if ((threadIdx.x & 31) == 0) atomicMin(&smin, m);
-    __syncthreads();
-    const int pi = smin == INT_MAX ? 0 : bitlen32(smin) - 1;
-    int64_t w = 0;
-    for (int t = threadIdx.x; t < total; t += 256) {
-        const int64_t at = index(t);
-        const int S = a.stats[at].y;
-        if (S > 0) w = max(w, attn_bound(attn_rho(S, pi), a.tmax[at], a.row[at].y));
-    }
-    atomicMax(&wmax, (unsigned long long)w);
-    __syncthreads();
-    if (threadIdx.x == 0) a.blk[(int64_t)bg * gridDim.x + J] = make_int2(pi, max(0, 64 - __clzll((long long)wmax) - 14));
-}
-
-// dK and dV, one warp per key
-__global__ void __launch_bounds__(128) attn_dkv_simple(const __grid_constant__ AttnArgs a) {
-    __shared__ int sp[4][32], ss[4][32];
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int64_t r = (int64_t)blockIdx.x * 4 + wp;
-    if (r >= (int64_t)a.B * a.Hkv * a.Lk) return;
-    const int j = (int)(r % a.Lk), bg = (int)(r / a.Lk), g = bg % a.Hkv, b = bg / a.Hkv;
-    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk);
-    const int i0 = a.causal ? max(0, j - (nk - nq)) : 0;
-    const int nv = a.Dp / 16;
-    const uint4 *kr = copy_row(a, OPK, b, g, j), *vr = copy_row(a, OPV, b, g, j);
-    const int2 pc = a.blk[(int64_t)bg * ((a.Lk + kKeyBlock - 1) / kKeyBlock) + j / kKeyBlock];
-    const float f = attn_factor(a, bg), sc = pow2f(-pc.y);
-    int64_t ak[4] = {0, 0, 0, 0}, av[4] = {0, 0, 0, 0};
-    for (int h = g * a.rep; h < (g + 1) * a.rep && j < nk; ++h)
-        for (int t0 = i0; t0 < nq; t0 += 32) {
-            const int i = t0 + lane;
-            int P = 0, U = 0;
-            if (i < nq) {
-                const int64_t at = ((int64_t)b * a.Hq + h) * a.Lq + i;
-                const int2 st = a.stats[at];
-                const int s = dot_row(copy_row(a, OPQ, b, h, i), kr, nv);
-                const float E = attn_weight((float)(s - st.x), f) - kAttnMagic;
-                const float p = __fmaf_rn(E, attn_rho(st.y, pc.x), kAttnMagic);
-                const int x = dot_row(copy_row(a, OPD, b, h, i), vr, nv) - a.row[at].x;
-                P = __float_as_int(p) - 0x4B400000;
-                U = __float_as_int(__fmaf_rn((p - kAttnMagic) * sc, (float)x, kAttnMagic)) - 0x4B400000;
-            }
-            sp[wp][lane] = P;
-            ss[wp][lane] = U;
-            __syncwarp();
-            for (int k = 0; k < 32 && t0 + k < nq; ++k) {
-                const int8_t *qd = reinterpret_cast<const int8_t *>(copy_row(a, OPQ, b, h, t0 + k));
-                const int8_t *dd = reinterpret_cast<const int8_t *>(copy_row(a, OPD, b, h, t0 + k));
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (c * 32 + lane < a.Dp) {
-                        av[c] += (int64_t)sp[wp][k] * dd[c * 32 + lane];
-                        ak[c] += (int64_t)ss[wp][k] * qd[c * 32 + lane];
-                    }
-            }
-            __syncwarp();
-        }
-    const int64_t row = (int64_t)b * a.Lk + j;
-    const int ed = attn_top(a, OPD, bg), ev = attn_top(a, OPV, bg), eq = attn_top(a, OPQ, bg);
-    store_row(a, a.dv, row, g, av, 1.0, ed - pc.x);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) ak[c] *= a.mul;
-    store_row(a, a.dk, row, g, ak, 1.0, pc.y - pc.x - a.shift + ed + ev + eq);
 }
 
 // ------------------------------------------------------------------ host
@@ -322,7 +148,7 @@ int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
 }
 
 struct Scratch {
-    size_t top, copy[OPN], row, tmax, blk, total;
+    size_t top, copy[OPN], row, tmax, total;
 };
 Scratch scratch(const AttnArgs &a, bool back) {
     Scratch s;
@@ -340,7 +166,6 @@ Scratch scratch(const AttnArgs &a, bool back) {
     s.copy[OPD] = take(back ? q * a.Dp : 0);
     s.row = take(back ? q * 8 : 0);
     s.tmax = take(back ? q * 4 : 0);
-    s.blk = take(back ? (int64_t)a.B * a.Hkv * host::cdiv(std::max(a.Lk, 1), kKeyBlock) * 8 : 0);
     s.total = at;
     return s;
 }
@@ -409,6 +234,45 @@ int launch_fwd(const AttnArgs &a, cudaStream_t s) {
     return host::launch_status();
 }
 
+template <typename K>
+int allow_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? ICT_OK : ICT_ERR_CUDA;
+}
+
+template <int DP>
+int launch_bwd(const AttnArgs &a, cudaStream_t s) {
+    CUtensorMap q, k, v, d;
+    int st;
+    if ((st = copy_map(&q, a, OPQ)) || (st = copy_map(&k, a, OPK)) || (st = copy_map(&v, a, OPV)) || (st = copy_map(&d, a, OPD)))
+        return st;
+    AttnLimits lim;
+    host::wait_limits(&lim.wait_ns, &lim.drain_ns);
+    const int64_t rows = (int64_t)a.B * a.Hq * a.Lq;
+    if (rows > 0) {
+        using L = DqCfg<DP>;
+        constexpr int NL = DP / 16;
+        attn_row_kernel<NL><<<(unsigned)host::cdiv(rows, 256 / NL), 256, 0, s>>>(a);
+        if ((st = allow_smem(attn_dq_kernel<DP>, L::kBytes))) return st;
+        attn_dq_kernel<DP><<<(unsigned)(host::cdiv(a.Lq, kQTile) * a.B * a.Hq), L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+        host::counted(2);
+    }
+    if ((int64_t)a.B * a.Lk > 0) {
+        using L = DkvCfg<DP>;
+        const unsigned blocks = (unsigned)(host::cdiv(a.Lk, kKeyBlock) * a.B * a.Hkv);
+        if constexpr (DP == 64) {
+            if ((st = allow_smem(attn_dkv_kernel<64, 3>, L::kBytes))) return st;
+            attn_dkv_kernel<64, 3><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+            host::counted(1);
+        } else {
+            if ((st = allow_smem(attn_dkv_kernel<DP, 1>, L::kBytes)) || (st = allow_smem(attn_dkv_kernel<DP, 2>, L::kBytes))) return st;
+            attn_dkv_kernel<DP, 2><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+            attn_dkv_kernel<DP, 1><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+            host::counted(2);
+        }
+    }
+    return host::launch_status();
+}
+
 }  // namespace
 
 namespace host {
@@ -473,23 +337,12 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     output(a.dv, dV, d->v_col);
     a.row = (int2 *)(base + w.row);
     a.tmax = (int32_t *)(base + w.tmax);
-    a.blk = (int2 *)(base + w.blk);
     if (rq == 0 && rk == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t rows = rq * a.Hq;
     host::Timer kt(s, ICT_KC_GEMM, 10.0 * (double)rows * a.Lk * a.D);
     if ((st = align_operands(a, s))) return st;
-    if (rows > 0) {
-        attn_row_kernel<<<(unsigned)host::cdiv(rows, 8), 256, 0, s>>>(a);
-        attn_dq_simple<<<(unsigned)host::cdiv(rows, 4), 128, 0, s>>>(a);
-        host::counted(2);
-    }
-    if (rk > 0) {
-        attn_block_kernel<<<dim3((unsigned)host::cdiv(a.Lk, kKeyBlock), (unsigned)(a.B * a.Hkv)), 256, 0, s>>>(a);
-        attn_dkv_simple<<<(unsigned)host::cdiv(rk * a.Hkv, 4), 128, 0, s>>>(a);
-        host::counted(2);
-    }
-    return host::launch_status();
+    return a.Dp == 64 ? launch_bwd<64>(a, s) : launch_bwd<128>(a, s);
 }
 
 }  // extern "C"

@@ -43,7 +43,6 @@ struct AttnArgs {
     int o_ngc, o_gv;
     int2 *row;           // [B * Hq * Lq]: delta', X
     int32_t *tmax;       // [B * Hq * Lq]: largest |T| of the row
-    int2 *blk;           // [B * Hkv][key blocks]: pi, c
     AttnOut dk, dv;
 };
 
@@ -60,17 +59,6 @@ __device__ __forceinline__ float attn_factor(const AttnArgs &a, int bg) {
     const int x = attn_top(a, OPQ, bg) + attn_top(a, OPK, bg) - a.shift - 23;
     return a.fmul * pow2f(min(max(x, -120), 60));
 }
-// E = RNE(2^14 2^(k / 64)), k = RNE((s - smax) f), as the float 1.5 2^23 + E.  The FMA onto
-// 1.5 2^17 rounds the exact product once to a multiple of 2^-6.  There are 1024 arguments
-// with a result above zero and ex2.approx rounds to the right whole number at all of them
-// (the GPU tests run through every one).
-__device__ __forceinline__ float attn_weight(float n_neg, float f64th) {
-    const float y = __fmaf_rn(n_neg, f64th, kGridMagic) - kGridMagic;
-    float z;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(y));
-    return __fmaf_rn(z, 16384.0f, kAttnMagic);
-}
-
 // quotient n / d as a group member: q = n / d rounded to 53 bits decides every rounding to
 // 8 bits as the exact quotient does, since n < 2^48 and d < 2^31 keep an inexact quotient
 // at least 2^-48 away (relatively) from every border between two mantissas
@@ -79,10 +67,6 @@ __device__ __forceinline__ int need_quot(double q) {  // q > 0
     return (int)(b >> 52) - 1023 - 6 + ((b & 0xFFFFFFFFFFFFFull) >= 0xFE00000000000ull ? 1 : 0);
 }
 __device__ __forceinline__ double pow2d(int k) { return __longlong_as_double((int64_t)(k + 1023) << 52); }
-__device__ __forceinline__ int quot_mant(double q, int S) {  // RNE(q 2^-S), saturated
-    const int v = __double2int_rn(q * pow2d(-S));
-    return v > 127 ? 127 : (v < -127 ? -127 : v);
-}
 
 // ---- pairs of fp32 values: one instruction works on both halves of a 64-bit register
 typedef unsigned long long f2;
@@ -109,16 +93,20 @@ __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     return r;
 }
 
-// The bit patterns 0x4B400000 + E of two weights from two scores: bias = 0x4B400000 - smax
-// (mod 2^32), so that the integer sum is the float 1.5 2^23 + (s - smax) itself.
-__device__ __forceinline__ void attn_weight2(uint32_t s0, uint32_t s1, uint32_t bias, f2 f64th, float &w0, float &w1) {
-    const f2 n = add2(pk(__uint_as_float(s0 + bias), __uint_as_float(s1 + bias)), pk(-kAttnMagic));
+// Two weights E = RNE(2^14 2^(k / 64)), k = RNE((s - smax) f), as the floats 1.5 2^23 + E.  The
+// FMA onto 1.5 2^17 rounds the exact product once to a multiple of 2^-6; there are 960
+// arguments with a result above zero, and ex2.approx rounds to the right whole number at all
+// of them (the GPU tests run through every one).
+//  s + 0x4B400000 is the bit pattern of 1.5 2^23 + s
+// (|s| < 2^21), and adding nm = -(1.5 2^23 + smax) leaves s - smax, both exact.
+__device__ __forceinline__ f2 attn_weight2f(uint32_t s0, uint32_t s1, f2 nm, f2 f64th) {
+    const f2 n = add2(pk(__uint_as_float(s0 + 0x4B400000u), __uint_as_float(s1 + 0x4B400000u)), nm);
     const f2 y = add2(fma2(n, f64th, pk(kGridMagic)), pk(-kGridMagic));
     float a, b;
     unpk(y, a, b);
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
-    unpk(fma2(pk(a, b), pk(16384.0f), pk(kAttnMagic)), w0, w1);
+    return fma2(pk(a, b), pk(16384.0f), pk(kAttnMagic));
 }
 // low and second bytes of four words
 __device__ __forceinline__ void split_bytes(float a, float b, float c, float d, uint32_t &lo, uint32_t &hi) {

@@ -161,14 +161,14 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
 // 32 scores of a row to the two byte planes of their weights; PART: only the first `vis`
 // columns are visible.  sum collects the bit patterns (1.5 2^23 + E each, mod 2^32).
 template <bool PART>
-__device__ __forceinline__ void weights32(const uint32_t (&v)[32], uint32_t bias, f2 f, int vis, uint32_t &sum,
+__device__ __forceinline__ void weights32(const uint32_t (&v)[32], f2 nm, f2 f, int vis, uint32_t &sum,
                                           uint32_t (&lo)[8], uint32_t (&hi)[8]) {
     uint32_t s0 = 0, s1 = 0;
 #pragma unroll
     for (int q = 0; q < 32; q += 4) {
         float w[4];
-        attn_weight2(v[q], v[q + 1], bias, f, w[0], w[1]);
-        attn_weight2(v[q + 2], v[q + 3], bias, f, w[2], w[3]);
+        unpk(attn_weight2f(v[q], v[q + 1], nm, f), w[0], w[1]);
+        unpk(attn_weight2f(v[q + 2], v[q + 3], nm, f), w[2], w[3]);
         if (PART) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) w[k] = q + k < vis ? w[k] : kAttnMagic;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             mx = max(mx, red[(wg ^ 1) * 128 + et]);
         }
         if (see == 0) mx = 0;
-        const uint32_t bias = 0x4B400000u - (uint32_t)mx;
+        const f2 nm = pk(-(kAttnMagic + (float)mx));
         const f2 f = pk(attn_factor(a, b * a.Hkv + g));
         uint32_t sum = 0;
         int n_sum = 0;
@@ -421,8 +421,8 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
                     uint32_t v[32];
                     tmem_ld32(mine + c, v);
                     tmem_ld_done(v);
-                    if (col + 32 <= see_min) weights32<false>(v, bias, f, 0, sum, lo, hi);
-                    else weights32<true>(v, bias, f, see - col, sum, lo, hi);
+                    if (col + 32 <= see_min) weights32<false>(v, nm, f, 0, sum, lo, hi);
+                    else weights32<true>(v, nm, f, see - col, sum, lo, hi);
                     n_sum += 32;
                 } else {
 #pragma unroll
