@@ -228,8 +228,11 @@ int launch_fwd(const AttnArgs &a, cudaStream_t s) {
         return ICT_ERR_CUDA;
     AttnLimits lim;
     host::wait_limits(&lim.wait_ns, &lim.drain_ns);
-    const int64_t blocks = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
-    attn_fwd_kernel<DP><<<(unsigned)blocks, L::kThreads, L::kBytes, s>>>(q, k, v, a, lim);
+    int sms = 0;
+    if ((st = host::device_info(&sms))) return st;
+    const int64_t items = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
+    const unsigned blocks = (unsigned)std::min<int64_t>(items, (int64_t)sms * (DP == 64 ? 2 : 1));
+    attn_fwd_kernel<DP><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, a, lim, (int)items);
     host::counted(1);
     return host::launch_status();
 }

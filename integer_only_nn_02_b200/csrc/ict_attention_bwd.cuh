@@ -29,7 +29,7 @@ constexpr int kSoftWarps = 16;
 // One step's 16 columns of T (two byte planes), the row's query in this thread.
 template <bool PART>
 __device__ __forceinline__ void dq16(const uint32_t (&vs)[16], const uint32_t (&vd)[16], f2 nm, f2 nd, f2 f, f2 sc, int vis,
-                                     int &tmax, int &tmin, uint32_t *lo, uint32_t *hi) {
+                                     int &tmax, int &tmin, uint32_t (&lo)[4], uint32_t (&hi)[4]) {
     const f2 M = pk(kAttnMagic), nM = pk(-kAttnMagic);
 #pragma unroll
     for (int q = 0; q < 16; q += 4) {
@@ -57,7 +57,8 @@ __device__ __forceinline__ void dq16(const uint32_t (&vs)[16], const uint32_t (&
 // (64 floats each).  PART: queries before `first` do not see the key.  MODE bit 0: dV, bit 1: dK.
 template <bool PART, int MODE>
 __device__ __forceinline__ void dkv16(const uint32_t (&vs)[16], const uint32_t (&vd)[16], const float *vec, f2 f, f2 sc,
-                                      int first, uint32_t *plo, uint32_t *phi, uint32_t *ulo, uint32_t *uhi) {
+                                      int first, uint32_t (&plo)[4], uint32_t (&phi)[4], uint32_t (&ulo)[4],
+                                      uint32_t (&uhi)[4]) {
     const f2 M = pk(kAttnMagic), nM = pk(-kAttnMagic);
 #pragma unroll
     for (int q = 0; q < 16; q += 4) {
@@ -268,26 +269,21 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             tc_fence_after();
             const int col = u * kStep + c0;
             if (c0 < most - u * kStep) {
-                uint32_t lo[8], hi[8];
                 const uint32_t mine = tm + lanes + pair * 128 + c0;
-                if (col < see_max) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
+                    if (col + c < see_max) {
                         uint32_t vs[16], vd[16];
-                        tmem_ld16(mine + 16 * k, vs);
-                        tmem_ld16(mine + kStep + 16 * k, vd);
+                        tmem_ld16(mine + c, vs);
+                        tmem_ld16(mine + kStep + c, vd);
                         tmem_ld_done(vs, vd);
-                        if (col + 16 * k + 16 <= see_min)
-                            dq16<false>(vs, vd, nm, nd, f, sc, 0, tmax, tmin, lo + 4 * k, hi + 4 * k);
-                        else
-                            dq16<true>(vs, vd, nm, nd, f, sc, see - col - 16 * k, tmax, tmin, lo + 4 * k, hi + 4 * k);
+                        if (col + c + 16 <= see_min) dq16<false>(vs, vd, nm, nd, f, sc, 0, tmax, tmin, lo, hi);
+                        else dq16<true>(vs, vd, nm, nd, f, sc, see - col - c, tmax, tmin, lo, hi);
                     }
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) lo[q] = hi[q] = 0;
+                    tmem_st4(mine + c / 4, hi);  // in the place of scores already read
+                    tmem_st4(mine + 8 + c / 4, lo);
                 }
-                tmem_st8(mine, hi);
-                tmem_st8(mine + 8, lo);
                 tmem_st_wait();
             }
             warp_arrive(bar_ef + 8 * pair);
@@ -595,28 +591,24 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const float *vec = (const float *)(smem + L::kOffVec) + (u & 3) * 3 * kStep + c0;
             const int i = base + k_in * kStep + c0;
             const uint32_t mine = tm + lanes + pair * 128 + c0;
-            uint32_t plo[8], phi[8], ulo[8], uhi[8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t vs[16], vd[16];
-                tmem_ld16(mine + 16 * k, vs);
-                if (MODE & 2) tmem_ld16(mine + kStep + 16 * k, vd);
+#pragma unroll 1
+            for (int c = 0; c < 32; c += 16) {
+                uint32_t vs[16], vd[16], plo[4], phi[4], ulo[4], uhi[4];
+                tmem_ld16(mine + c, vs);
+                if (MODE & 2) tmem_ld16(mine + kStep + c, vd);
                 tmem_ld_wait();
                 tmem_tie(vs);
                 if (MODE & 2) tmem_tie(vd);
-                if (i + 16 * k >= lo_max)
-                    dkv16<false, MODE>(vs, vd, vec + 16 * k, f, sc, 0, plo + 4 * k, phi + 4 * k, ulo + 4 * k, uhi + 4 * k);
-                else
-                    dkv16<true, MODE>(vs, vd, vec + 16 * k, f, sc, lo_i - i - 16 * k, plo + 4 * k, phi + 4 * k, ulo + 4 * k,
-                                      uhi + 4 * k);
-            }
-            if (MODE & 1) {
-                tmem_st8(mine, phi);
-                tmem_st8(mine + 8, plo);
-            }
-            if (MODE & 2) {
-                tmem_st8(mine + kStep, uhi);
-                tmem_st8(mine + kStep + 8, ulo);
+                if (i + c >= lo_max) dkv16<false, MODE>(vs, vd, vec + c, f, sc, 0, plo, phi, ulo, uhi);
+                else dkv16<true, MODE>(vs, vd, vec + c, f, sc, lo_i - i - c, plo, phi, ulo, uhi);
+                if (MODE & 1) {  // in the place of scores already read
+                    tmem_st4(mine + c / 4, phi);
+                    tmem_st4(mine + 8 + c / 4, plo);
+                }
+                if (MODE & 2) {
+                    tmem_st4(mine + kStep + c / 4, uhi);
+                    tmem_st4(mine + kStep + 8 + c / 4, ulo);
+                }
             }
             tmem_st_wait();
             warp_arrive(bar_ef + 8 * pair);
