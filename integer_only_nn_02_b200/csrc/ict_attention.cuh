@@ -137,6 +137,15 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N], uint32_t (&w)[N])
     tmem_tie(w);
 }
 
+// mbar_wait with its waiting loop out of line: these kernels wait at some 30 places, and inlined
+// loops push the softmax code out of the instruction caches.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint64_t limit_ns, const volatile int *abort) {
+    return mbar_wait(bar, parity, limit_ns, abort);
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns, const volatile int *abort) {
+    return mbar_try_wait(bar, parity) || wait_slow(bar, parity, limit_ns, abort);
+}
+
 // One arrival per warp once all its lanes are here (their TMEM reads waited for): an arrival
 // per thread costs a serial shared-memory atomic each.
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {

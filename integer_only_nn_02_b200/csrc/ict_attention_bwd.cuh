@@ -165,8 +165,8 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             int n = 0;
             for (int t = 0; t < nt; ++t) {
                 const int s = t % L::KS, v = t % L::VS;
-                if (t >= L::KS && !mbar_wait(bar_ke + 8 * s, (t / L::KS - 1) & 1, lim.wait_ns, abort_flag)) ok = false;
-                if (ok && t >= L::VS && !mbar_wait(bar_ve + 8 * v, (t / L::VS - 1) & 1, lim.wait_ns, abort_flag)) ok = false;
+                if (t >= L::KS && !wait_bar(bar_ke + 8 * s, (t / L::KS - 1) & 1, lim.wait_ns, abort_flag)) ok = false;
+                if (ok && t >= L::VS && !wait_bar(bar_ve + 8 * v, (t / L::VS - 1) & 1, lim.wait_ns, abort_flag)) ok = false;
                 if (!ok) break;
                 mbar_expect_tx(bar_kf + 8 * s, L::kTile);
                 load_tile(&tmK, sb + L::kOffK + s * L::kTile, bar_kf + 8 * s, krow + t * 128);
@@ -175,11 +175,11 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
                 ++n;
             }
             if (!ok) fail();
-            mbar_wait(bar_q, 0, lim.drain_ns, nullptr);
+            wait_bar(bar_q, 0, lim.drain_ns, nullptr);
             for (int t = max(0, n - L::KS); t < n; ++t)
-                mbar_wait(bar_kf + 8 * (t % L::KS), (t / L::KS) & 1, lim.drain_ns, nullptr);
+                wait_bar(bar_kf + 8 * (t % L::KS), (t / L::KS) & 1, lim.drain_ns, nullptr);
             for (int t = max(0, n - L::VS); t < n; ++t)
-                mbar_wait(bar_vf + 8 * (t % L::VS), (t / L::VS) & 1, lim.drain_ns, nullptr);
+                wait_bar(bar_vf + 8 * (t % L::VS), (t / L::VS) & 1, lim.drain_ns, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             constexpr uint32_t kIdHi = idesc_i8(128, DP, false, true);              // signed high plane
             constexpr uint32_t kIdLo = idesc_i8(128, DP, false, true) & ~(1u << 7);  // unsigned low plane
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, lim.wait_ns, abort_flag));
+                return (bool)__all_sync(0xffffffffu, wait_bar(bar, parity, lim.wait_ns, abort_flag));
             };
             bool ok = wait(bar_q, 0);
             // S and dP of step u into buffer u & 1
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
                 umma_commit(bar_dr);
             }
             __syncwarp();
-            mbar_wait(bar_dr, 0, lim.drain_ns, nullptr);
+            wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
         }
     } else {
         // ------------------------------------------------------------ softmax
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
         int tmax = 0x4B400000, tmin = 0x4B400000;
         bool ok = true;
         for (int u = pair; u < nu && ok; u += 2) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_sf + 8 * pair, (u >> 1) & 1, lim.wait_ns, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, (u >> 1) & 1, lim.wait_ns, abort_flag));
             if (!ok) break;
             tc_fence_after();
             const int col = u * kStep + c0;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
         int *red = (int *)(smem + L::kOffRed + 8 * 128 * 8);
         red[wg * 128 + et] = max(tmax - 0x4B400000, 0x4B400000 - tmin);
         if (nt > 0 && ok) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_of, 0, lim.wait_ns, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_bar(bar_of, 0, lim.wait_ns, abort_flag));
             tc_fence_after();
         }
         if (!ok && lane == 0) fail();
@@ -300,16 +300,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
         const int cc = wg * (DP / 4);
         fit_row_tmem<DP / 64>(a, a.o, (int64_t)b * a.Lq + i, h, cc, read ? st.y : 0, a.mul,
                               tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
-                              nk <= 1024, gm, 128, 1, 32 * kSoftWarps, [&](int s, uint32_t(&hi)[16], uint32_t(&lo)[16]) {
-                                  if (read) {
-                                      tmem_ld16(tm + lanes + kAccCol + cc + s * 16, hi);
-                                      tmem_ld16(tm + lanes + kAccCol + DP + cc + s * 16, lo);
-                                      tmem_ld_done(hi, lo);
-                                  } else {
-#pragma unroll
-                                      for (int q = 0; q < 16; ++q) hi[q] = lo[q] = 0;
-                                  }
-                              });
+                              nk <= 1024, gm, 128, 1, 32 * kSoftWarps, AccCols{tm + lanes + kAccCol, DP, read});
         if (wg == 0 && live) a.tmax[at] = max(max(red[et], red[128 + et]), max(red[256 + et], red[384 + et]));
     }
     tc_fence_before();
@@ -440,7 +431,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             int w = 0;
             for (; w < nw; ++w) {
                 const int s = w % L::QS;
-                if (w >= L::QS && !mbar_wait(bar_qe + 8 * s, (w / L::QS - 1) & 1, lim.wait_ns, abort_flag)) {
+                if (w >= L::QS && !wait_bar(bar_qe + 8 * s, (w / L::QS - 1) & 1, lim.wait_ns, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -451,9 +442,9 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 load_tile(&tmD, dst + L::kTile, bar_qf + 8 * s, row);
             }
             if (!ok) fail();
-            mbar_wait(bar_k, 0, lim.drain_ns, nullptr);
+            wait_bar(bar_k, 0, lim.drain_ns, nullptr);
             for (int t = max(0, w - L::QS); t < w; ++t)
-                mbar_wait(bar_qf + 8 * (t % L::QS), (t / L::QS) & 1, lim.drain_ns, nullptr);
+                wait_bar(bar_qf + 8 * (t % L::QS), (t / L::QS) & 1, lim.drain_ns, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -462,7 +453,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             constexpr uint32_t kIdHi = idesc_i8(128, DP, false, true);
             constexpr uint32_t kIdLo = idesc_i8(128, DP, false, true) & ~(1u << 7);
             auto wait = [&](uint32_t bar, uint32_t parity) {
-                return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, lim.wait_ns, abort_flag));
+                return (bool)__all_sync(0xffffffffu, wait_bar(bar, parity, lim.wait_ns, abort_flag));
             };
             bool ok = wait(bar_k, 0);
             // walk of the steps: tile index w and half within the tile, for the scores and for the products
@@ -534,7 +525,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 umma_commit(bar_dr);
             }
             __syncwarp();
-            mbar_wait(bar_dr, 0, lim.drain_ns, nullptr);
+            wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
         }
     } else if (warp == kSoftWarps + 2) {
         // ------------------------------------------------------------ the queries' vectors
@@ -565,7 +556,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             }
             fetch(u + 1);
             const int s = u & 3;
-            if (u >= 4) ok = __all_sync(0xffffffffu, mbar_wait(bar_ce + 8 * s, ((u >> 2) - 1) & 1, lim.wait_ns, abort_flag));
+            if (u >= 4) ok = __all_sync(0xffffffffu, wait_bar(bar_ce + 8 * s, ((u >> 2) - 1) & 1, lim.wait_ns, abort_flag));
             float *v = (float *)(smem + L::kOffVec) + s * 3 * kStep + 2 * lane;
             *reinterpret_cast<float2 *>(v) = make_float2(m[0], m[1]);
             *reinterpret_cast<float2 *>(v + kStep) = make_float2(r[0], r[1]);
@@ -584,8 +575,8 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         bool ok = true;
         int k_in = pair % max(per, 1);
         for (int u = pair; u < nu && ok; u += 2) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_sf + 8 * pair, (u >> 1) & 1, lim.wait_ns, abort_flag) &&
-                                             mbar_wait(bar_cf + 8 * (u & 3), (u >> 2) & 1, lim.wait_ns, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, (u >> 1) & 1, lim.wait_ns, abort_flag) &&
+                                             wait_bar(bar_cf + 8 * (u & 3), (u >> 2) & 1, lim.wait_ns, abort_flag));
             if (!ok) break;
             tc_fence_after();
             const float *vec = (const float *)(smem + L::kOffVec) + (u & 3) * 3 * kStep + c0;
@@ -616,7 +607,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             if ((k_in += 2) >= per) k_in %= per;
         }
         if (nu > 0 && ok) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_of, 0, lim.wait_ns, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_bar(bar_of, 0, lim.wait_ns, abort_flag));
             tc_fence_after();
         }
         if (!ok && lane == 0) fail();
@@ -627,22 +618,12 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         const int cc = MODE == 3 ? (wg & 1) * 32 : wg * 32, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
         float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 8 * 128 : 0) + et;
         const int64_t row = (int64_t)b * a.Lk + j;
-        auto load = [&](int s, uint32_t(&hi)[16], uint32_t(&lo)[16]) {
-            if (read) {
-                tmem_ld16(tm + lanes + acc + cc + s * 16, hi);
-                tmem_ld16(tm + lanes + acc + DP + cc + s * 16, lo);
-                tmem_ld_done(hi, lo);
-            } else {
-#pragma unroll
-                for (int q = 0; q < 16; ++q) hi[q] = lo[q] = 0;
-            }
-        };
         const int den = read && j < nk ? 1 : 0;
         const bool narrow = (int64_t)nq * a.rep <= 1024;
         const int bar = MODE == 3 ? 1 + (wg >> 1) : 1, nthr = MODE == 3 ? 256 : 32 * kSoftWarps;
         const AttnOut &out = is_k ? a.dk : a.dv;
         const int mul = is_k ? a.mul : 1, r = is_k ? cexp - pi - a.shift + ed + ev + eq : ed - pi;
-        fit_row_tmem<2>(a, out, row, g, cc, den, mul, r, live, narrow, gm, 128, bar, nthr, load);
+        fit_row_tmem<2>(a, out, row, g, cc, den, mul, r, live, narrow, gm, 128, bar, nthr, AccCols{tm + lanes + acc, DP, read});
     }
     tc_fence_before();
     __syncthreads();

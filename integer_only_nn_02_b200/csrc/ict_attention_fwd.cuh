@@ -64,35 +64,49 @@ __device__ __forceinline__ double acc_f64(uint32_t hi, uint32_t lo) {
     return (double)((int64_t)(int)hi * 256 + (int)lo);
 }
 
-// 16 mantissas RNE(n rden) of accumulators n, from v = fma(n, sc, 1.5 2^23) in fp32: where the
-// fp32 value lies within its error bound of a border between two mantissas (near, a mask of
-// this thread's columns), that column is decided in fp64.
-__device__ __forceinline__ void settle16(uint32_t (&v)[16], uint32_t near, bool capped, double rden, const uint32_t (&hi)[16],
-                                         const uint32_t (&lo)[16]) {
-    if (capped) near = 0xffff;
+// Where a row's accumulators lie: TMEM address of column 0's high plane (this warp's lanes), the
+// low plane `lo` columns on; nothing there (all zero) where on = false.
+struct AccCols {
+    uint32_t hi;
+    int lo;
+    bool on;
+    __device__ __forceinline__ void load16(int c, uint32_t (&h)[16], uint32_t (&l)[16]) const {
+        if (on) {
+            tmem_ld16(hi + c, h);
+            tmem_ld16(hi + lo + c, l);
+            tmem_ld_done(h, l);
+        } else {
 #pragma unroll
-    for (int q = 0; q < 16; ++q)
-        if (near >> q & 1) {
-            const double n = acc_f64(hi[q], lo[q]);
-            v[q] = (uint32_t)(capped ? (int)fmin(fmax(n * rden, -127.0), 127.0) : quot_mant_fast(n, rden));
+            for (int q = 0; q < 16; ++q) h[q] = l[q] = 0;
         }
-}
+    }
+    __device__ __forceinline__ double exact(int c) const {  // column c as a whole number
+        uint32_t h[1] = {0}, l[1] = {0};
+        if (on) {
+            h[0] = tmem_ld1(hi + c);
+            l[0] = tmem_ld1(hi + lo + c);
+            tmem_ld_done(h, l);
+        }
+        return acc_f64(h[0], l[0]);
+    }
+};
 
 // FIT of one row's accumulators (this thread's TMEM lane): quotients (256 hi + lo) mul / den at
 // exponent r, SEGS segments of 16 columns from column c0 of head h.  The threads that share a
 // row join their segments' maxima in gmax (shared memory, [segment][stride], two floats each).
 // Magnitudes and mantissas are computed in fp32 with an error bound; what lies within the bound
-// of a border between two results is decided in fp64, where the quotient's rounding to 53 bits
-// cannot hide the border.  narrow: the accumulators 256 hi + lo fit 32 bits.
-template <int SEGS, typename Load>
+// of a border between two results (a mantissa in some ten thousand) is read again and decided
+// in fp64, where the quotient's rounding to 53 bits cannot hide the border.  narrow: the
+// accumulators 256 hi + lo fit 32 bits.
+template <int SEGS>
 __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &out, int64_t row, int h, int c0, int den,
                                              int mul, int r, bool live, bool narrow, float2 *gmax, int stride, int bar,
-                                             int nthreads, const Load &load) {
+                                             int nthreads, const AccCols &acc) {
     const int col = out.col + h * a.D;
 #pragma unroll 1
     for (int s = 0; s < SEGS; ++s) {
         uint32_t hi[16], lo[16];
-        load(s, hi, lo);
+        acc.load16(c0 + 16 * s, hi, lo);
         float m = 0, w = 0;
         if (narrow) {
             int mi = 0;
@@ -135,15 +149,10 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
             const int n1 = zero ? 0 : need_rel_f32(__float_as_uint(q0 + dq), 8);
             int need = n1;
             bool none = zero;
-            if (__any_sync(0xffffffffu, n0 != n1)) {
-                // exact: the largest magnitude as a whole number, from this thread's and the other's columns
+            if (__any_sync(0xffffffffu, n0 != n1)) {  // exact: the largest magnitude as a whole number
                 double best = 0;
-                for (int k = g * gs; k < (g + 1) * gs; ++k) {
-                    uint32_t hi[16], lo[16];
-                    load(k - c0 / 16, hi, lo);
-#pragma unroll
-                    for (int q = 0; q < 16; ++q) best = fmax(best, fabs(acc_f64(hi[q], lo[q])));
-                }
+#pragma unroll 1
+                for (int c = g * out.G; c < (g + 1) * out.G; ++c) best = fmax(best, fabs(acc.exact(c)));
                 none = zero || best == 0;
                 if (!none) need = need_quot(best * (double)mul / (double)den);
             }
@@ -152,8 +161,8 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
             lim = fmaf(w * sc, -9.5367431640625e-07f, 0.4999999f);  // half a step less the bound: w sc 2^-20
             if (live && seg % gs == 0) out.exp[row * out.ngc + col / out.G + g] = (int8_t)e;
         }
-        uint32_t hi[16], lo[16], v[16];
-        load(s, hi, lo);
+        uint32_t hi[16], lo[16];
+        acc.load16(seg * 16, hi, lo);
         uint32_t near = 0;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -161,15 +170,31 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
             const float w = fmaf(n, sc, kAttnMagic);
             const float d = fmaf(n, sc, kAttnMagic - w);  // what the rounding took away
             if (!(fabsf(d) < lim)) near |= 1u << q;
-            v[q] = __float_as_uint(w);
+            hi[q] = __float_as_uint(w);
         }
+        uint32_t w0 = pack4b(hi[0], hi[1], hi[2], hi[3]), w1 = pack4b(hi[4], hi[5], hi[6], hi[7]);
+        uint32_t w2 = pack4b(hi[8], hi[9], hi[10], hi[11]), w3 = pack4b(hi[12], hi[13], hi[14], hi[15]);
         const bool capped = e == 127;
-        if (__any_sync(0xffffffffu, near != 0 || capped))
-            settle16(v, near, capped, e == kEZero || !some ? 0.0 : pow2d(r - e) * (double)mul / (double)den, hi, lo);
-        if (live)
-            *reinterpret_cast<uint4 *>(out.mant + row * out.ld + col + seg * 16) =
-                make_uint4(pack4b(v[0], v[1], v[2], v[3]), pack4b(v[4], v[5], v[6], v[7]),
-                           pack4b(v[8], v[9], v[10], v[11]), pack4b(v[12], v[13], v[14], v[15]));
+        if (capped) near = 0xffff;
+        uint32_t todo = __reduce_or_sync(0xffffffffu, near);
+        if (todo) {
+            const double rden = e == kEZero || !some ? 0.0 : pow2d(r - e) * (double)mul / (double)den;
+            while (todo) {
+                const int q = __ffs(todo) - 1;
+                todo &= todo - 1;
+                const double n = acc.exact(seg * 16 + q);
+                if (near >> q & 1) {
+                    const int v = capped ? (int)fmin(fmax(n * rden, -127.0), 127.0) : quot_mant_fast(n, rden);
+                    const uint32_t sh = 8 * (q & 3), keep = ~(0xffu << sh), put = (uint32_t)(v & 0xff) << sh;
+                    const int k = q >> 2;
+                    w0 = k == 0 ? (w0 & keep) | put : w0;
+                    w1 = k == 1 ? (w1 & keep) | put : w1;
+                    w2 = k == 2 ? (w2 & keep) | put : w2;
+                    w3 = k == 3 ? (w3 & keep) | put : w3;
+                }
+            }
+        }
+        if (live) *reinterpret_cast<uint4 *>(out.mant + row * out.ld + col + seg * 16) = make_uint4(w0, w1, w2, w3);
     }
 }
 
@@ -274,7 +299,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
                 for (int x = 0; x < H; ++x) tma_load_2d(dst + x * kHalfTile, m, bar, 64 * x, row);
             };
             auto free = [&](uint32_t bar, int n, int stages) {  // the n-th use of a ring's stage
-                return n < stages || mbar_wait(bar + 8 * (n % stages), (n / stages - 1) & 1, lim.wait_ns, abort_flag);
+                return n < stages || wait_bar(bar + 8 * (n % stages), (n / stages - 1) & 1, lim.wait_ns, abort_flag);
             };
             bool ok = true;
             int qn = 0, kn = 0, vn = 0;  // tiles issued so far
@@ -299,11 +324,11 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             if (!ok) fail();
             // every copy lands before the block may end
             for (int k = max(0, qn - L::QS); k < qn; ++k)
-                mbar_wait(bar_qf + 8 * (k % L::QS), (k / L::QS) & 1, lim.drain_ns, nullptr);
+                wait_bar(bar_qf + 8 * (k % L::QS), (k / L::QS) & 1, lim.drain_ns, nullptr);
             for (int k = max(0, kn - L::KS); k < kn; ++k)
-                mbar_wait(bar_kf + 8 * (k % L::KS), (k / L::KS) & 1, lim.drain_ns, nullptr);
+                wait_bar(bar_kf + 8 * (k % L::KS), (k / L::KS) & 1, lim.drain_ns, nullptr);
             for (int k = max(0, vn - L::VS); k < vn; ++k)
-                mbar_wait(bar_vf + 8 * (k % L::VS), (k / L::VS) & 1, lim.drain_ns, nullptr);
+                wait_bar(bar_vf + 8 * (k % L::VS), (k / L::VS) & 1, lim.drain_ns, nullptr);
         }
     } else if (warp == 4 * NWG + 1) {
         // ------------------------------------------------------------ TMEM and MMA issue
@@ -317,7 +342,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
         constexpr uint32_t kIdO = idesc_i8(128, DP, false, true) & ~(1u << 7);  // unsigned A
         constexpr int PER = 128 / L::TN;  // steps of a K or V tile
         auto wait = [&](uint32_t bar, int parity) {
-            return (bool)__all_sync(0xffffffffu, mbar_wait(bar, (uint32_t)(parity & 1), lim.wait_ns, abort_flag));
+            return (bool)__all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(parity & 1), lim.wait_ns, abort_flag));
         };
         bool ok = true;
         // uses so far: Q, K and V tiles, weights, outputs; and as bits (one per score buffer) the
@@ -407,7 +432,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
         if (!ok && lane == 0) fail();
         if (elect_one()) umma_commit(bar_dr);
         __syncwarp();
-        mbar_wait(bar_dr, 0, lim.drain_ns, nullptr);
+        wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
     } else {
         // ------------------------------------------------------------ softmax
         named_bar_sync(2, NS + 32);
@@ -420,7 +445,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
         uint32_t sf_par = 0;  // parity of the next phase of each score buffer, as bits
         bool ok = true;
         auto full = [&](int buf) {
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_sf + 8 * buf, (sf_par >> buf) & 1, lim.wait_ns, abort_flag));
+            ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * buf, (sf_par >> buf) & 1, lim.wait_ns, abort_flag));
             sf_par ^= 1u << buf;
             tc_fence_after();
             return ok;
@@ -433,7 +458,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             // pass 1: each warpgroup takes the tiles of one buffer
             int mx = INT_MIN;
             for (int t = wg; t < w.nt && ok; t += 2) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar_sf + 8 * wg, ((sf_par >> wg) + (t >> 1)) & 1, lim.wait_ns, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * wg, ((sf_par >> wg) + (t >> 1)) & 1, lim.wait_ns, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -499,7 +524,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             named_bar_sync(1, NS);
             sum += (uint32_t)red[256 + (wg ^ 1) * 128 + et];
             if (w.nt > 0 && ok) {
-                ok = __all_sync(0xffffffffu, mbar_wait(bar_of, on & 1, lim.wait_ns, abort_flag));
+                ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
                 tc_fence_after();
             }
             const bool live = i < a.Lq, read = w.nt > 0 && ok;
@@ -509,16 +534,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             float2 *gm = (float2 *)(smem + L::kOffRed + 2048) + et;
             fit_row_tmem<DP / NWG / 16>(
                 a, a.o, (int64_t)w.b * a.Lq + i, w.h, c0, read ? (int)sum : 0, 1, attn_top(a, OPV, w.b * a.Hkv + w.g), live,
-                w.nk <= 1024, gm, 128, 1, NS, [&](int s, uint32_t(&hi)[16], uint32_t(&lo)[16]) {
-                    if (read) {
-                        tmem_ld16(tm + lanes + L::kO + c0 + s * 16, hi);
-                        tmem_ld16(tm + lanes + L::kO + DP + c0 + s * 16, lo);
-                        tmem_ld_done(hi, lo);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) hi[q] = lo[q] = 0;
-                    }
-                });
+                w.nk <= 1024, gm, 128, 1, NS, AccCols{tm + lanes + L::kO, DP, read});
             if (w.nt > 0) {
                 warp_arrive(bar_oe);
                 ++on;
