@@ -14,49 +14,89 @@ namespace {
 
 // ------------------------------------------------------------------ aligned operands
 
-constexpr int kTopRows = 64;
-
-// Largest group exponent of every operand's valid rows, per sequence and key/value head.
-__global__ void __launch_bounds__(256) attn_top_kernel(const __grid_constant__ AttnArgs a) {
-    __shared__ int m[256];
-    const AttnOperand &o = a.op[blockIdx.z];
-    const int b = blockIdx.y, n = clamp_len(o.lens, b, o.L), l0 = blockIdx.x * kTopRows;
-    if (l0 >= n) return;
-    const int rows = min(kTopRows, n - l0), vecs = o.heads * (a.D / 16), per = vecs / a.Hkv;
-    for (int g = threadIdx.x; g < a.Hkv; g += 256) m[g] = kNoExp;
-    __syncthreads();
-    for (int t = threadIdx.x; t < rows * vecs; t += 256) {
-        const int l = t / vecs, v = t - l * vecs;
-        const int e = o.exp[((int64_t)b * o.L + l0 + l) * o.ngc + (o.col / 16 + v) / o.gv];
-        if (e != kEZero) atomicMax(&m[v / per], e);
+// Shared by the two kernels below: the rows [l0, l1) of one operand of one sequence and
+// key/value head.  A vector is 16 columns; vectors of one row lie side by side.
+struct OperandRows {
+    const AttnOperand &o;
+    int b, g, per, l0, l1, nvd;  // query heads of the group, rows, vectors of a head's columns
+    __device__ __forceinline__ int exponent(int l, int h, int v) const {
+        const int vec = o.col / 16 + h * nvd + v;
+        return o.exp[((int64_t)b * o.L + l) * o.ngc + (o.gsh >= 0 ? vec >> o.gsh : vec / o.gv)];
     }
+};
+
+// largest exponent of the rows' groups that are not zero, over the block
+__device__ __forceinline__ int block_top(const OperandRows &r, int *scratch) {
+    int m = kNoExp;
+    const int n = (r.l1 - r.l0) * r.nvd;
+    for (int k = 0; k < r.per; ++k)
+        for (int t = threadIdx.x; t < n; t += blockDim.x) {
+            const int l = t / r.nvd, e = r.exponent(r.l0 + l, r.g * r.per + k, t - l * r.nvd);
+            if (e != kEZero) m = max(m, e);
+        }
+    m = warp_max(m);
+    if (threadIdx.x == 0) *scratch = kNoExp;
     __syncthreads();
-    for (int g = threadIdx.x; g < a.Hkv; g += 256)
-        if (m[g] > kNoExp) atomicMax(&a.top[(blockIdx.z * a.B + b) * a.Hkv + g], m[g]);
+    if ((threadIdx.x & 31) == 0 && m > kNoExp) atomicMax(scratch, m);
+    __syncthreads();
+    return *scratch;
 }
 
-// Aligned copies [B][heads][L][Dp]: RNE(C 2^(e - e*)), zeros beyond the sequence's length
-// and the head's width.
-__global__ void __launch_bounds__(256) attn_copy_kernel(const __grid_constant__ AttnArgs a) {
-    const AttnOperand &o = a.op[blockIdx.y];
-    const int nv = a.Dp / 16;
-    const int64_t n = (int64_t)a.B * o.heads * o.L * nv;
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
-        const int v = (int)(t % nv);
-        const int64_t r = t / nv;
-        const int l = (int)(r % o.L);
-        const int bh = (int)(r / o.L), h = bh % o.heads, b = bh / o.heads;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (v < a.D / 16 && l < clamp_len(o.lens, b, o.L)) {
-            const int64_t row = (int64_t)b * o.L + l;
-            const int col = o.col + h * a.D + v * 16;
-            const int e = o.exp[row * o.ngc + (col / 16) / o.gv];
-            const int es = a.top[(blockIdx.y * a.B + b) * a.Hkv + h / (o.heads / a.Hkv)];
-            w = *reinterpret_cast<const uint4 *>(o.mant + row * o.ld + col);
-            w = rne_shift16(w, rne_index(es, e));
+// The rows' aligned copies [B][heads][L][Dp]: RNE(C 2^(e - e*)), zeros beyond the sequence's
+// length and the head's width.  rows: the copy's rows [l0, lend), of which [l0, l1) are valid.
+template <int NV>
+__device__ __forceinline__ void copy_rows(const AttnArgs &a, const OperandRows &r, int lend, int es) {
+    for (int k = 0; k < r.per; ++k) {
+        const int h = r.g * r.per + k;
+        int8_t *dst = r.o.copy + (((int64_t)r.b * r.o.heads + h) * r.o.L) * a.Dp;
+        const int8_t *src = r.o.mant + (int64_t)r.b * r.o.L * r.o.ld + r.o.col + h * a.D;
+        for (int t = threadIdx.x; t < (lend - r.l0) * NV; t += blockDim.x) {
+            const int l = r.l0 + t / NV, v = t % NV;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (l < r.l1 && v < r.nvd) {
+                w = *reinterpret_cast<const uint4 *>(src + (int64_t)l * r.o.ld + v * 16);
+                const int e = r.exponent(l, h, v);
+                if (e != es) w = rne_shift16(w, rne_index(es, e));
+            }
+            *reinterpret_cast<uint4 *>(dst + (int64_t)l * a.Dp + v * 16) = w;
         }
-        *reinterpret_cast<uint4 *>(o.copy + t * 16) = w;
     }
+}
+
+constexpr int kTopRows = 128;      // rows of a block of the two-kernel form
+constexpr int kFuseVecs = 8192;    // at most this many vectors per operand and key/value head: one kernel
+
+// Largest group exponent of every operand's valid rows, per sequence and key/value head
+// (a.top, very negative before).  Grid (row block, sequence and head, operand).
+__global__ void __launch_bounds__(256) attn_top_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ int m;
+    const AttnOperand &o = a.op[blockIdx.z];
+    const int bg = blockIdx.x, b = bg / a.Hkv, n = clamp_len(o.lens, b, o.L), l0 = blockIdx.y * kTopRows;
+    if (l0 >= n) return;
+    const int e = block_top(OperandRows{o, b, bg - b * a.Hkv, o.heads / a.Hkv, l0, min(n, l0 + kTopRows), a.D / 16}, &m);
+    if (threadIdx.x == 0 && e > kNoExp) atomicMax(&a.top[(blockIdx.z * a.B + b) * a.Hkv + bg % a.Hkv], e);
+}
+template <int NV>
+__global__ void __launch_bounds__(256) attn_copy_kernel(const __grid_constant__ AttnArgs a) {
+    const AttnOperand &o = a.op[blockIdx.z];
+    const int bg = blockIdx.x, b = bg / a.Hkv, n = clamp_len(o.lens, b, o.L), l0 = blockIdx.y * kTopRows;
+    if (l0 >= o.L) return;
+    const int lend = min(o.L, l0 + kTopRows);
+    copy_rows<NV>(a, OperandRows{o, b, bg - b * a.Hkv, o.heads / a.Hkv, l0, max(l0, min(n, lend)), a.D / 16}, lend,
+                  a.top[blockIdx.z * a.B * a.Hkv + bg]);
+}
+// Both in one kernel, a block per sequence, key/value head and operand: the exponents are
+// scanned by the block that copies.  One launch and one pass instead of a memset and two
+// launches; for heads of 197 x 64 the three operands of 768 heads take 11 us against 36 us.
+template <int NV>
+__global__ void __launch_bounds__(512) attn_align_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ int m;
+    const AttnOperand &o = a.op[blockIdx.y];
+    const int bg = blockIdx.x, b = bg / a.Hkv, n = clamp_len(o.lens, b, o.L);
+    const OperandRows r{o, b, bg - b * a.Hkv, o.heads / a.Hkv, 0, n, a.D / 16};
+    const int es = block_top(r, &m);
+    copy_rows<NV>(a, r, o.L, es);
+    if (threadIdx.x == 0) a.top[blockIdx.y * a.B * a.Hkv + bg] = es;
 }
 
 // ------------------------------------------------------------------ backward
@@ -172,6 +212,7 @@ Scratch scratch(const AttnArgs &a, bool back) {
 
 void operand(AttnOperand &o, const ict_tensor *t, int col, int heads, int L, const int32_t *lens, int8_t *copy) {
     o.mant = t->mant, o.exp = t->exp, o.ld = t->ld, o.ngc = groups_per_row(t), o.gv = vec_per_group(t);
+    o.gsh = (o.gv & (o.gv - 1)) == 0 ? __builtin_ctz((unsigned)o.gv) : -1;
     o.col = col, o.heads = heads, o.L = L, o.lens = lens, o.copy = copy;
 }
 void output(AttnOut &o, const ict_tensor *t, int col) {
@@ -201,12 +242,21 @@ int setup(AttnArgs &a, Scratch &w, const ict_attn_desc *d, bool back, const ict_
     return ICT_OK;
 }
 
+template <int NV>
 int align_operands(const AttnArgs &a, cudaStream_t s) {
-    if (cudaMemsetAsync(a.top, 0x80, (size_t)OPN * a.B * a.Hkv * 4, s) != cudaSuccess) return ICT_ERR_CUDA;
     const int L = std::max(a.Lq, a.Lk);
-    attn_top_kernel<<<dim3((unsigned)host::cdiv(L, kTopRows), (unsigned)a.B, (unsigned)a.n_op), 256, 0, s>>>(a);
-    const int64_t n = std::max((int64_t)a.Hq * a.Lq, (int64_t)a.Hkv * a.Lk) * a.B * (a.Dp / 16);
-    attn_copy_kernel<<<dim3((unsigned)std::min<int64_t>(host::cdiv(n, 256), 148 * 16), (unsigned)a.n_op), 256, 0, s>>>(a);
+    const int64_t vecs = std::max((int64_t)a.rep * a.Lq, (int64_t)a.Lk) * NV;
+    const unsigned bg = (unsigned)(a.B * a.Hkv);
+    // a few iterations per thread, or enough heads to fill the SMs
+    if (vecs <= kFuseVecs || (bg >= 148 && vecs <= 4 * kFuseVecs)) {
+        attn_align_kernel<NV><<<dim3(bg, (unsigned)a.n_op), 512, 0, s>>>(a);
+        host::counted(1);
+        return host::launch_status();
+    }
+    if (cudaMemsetAsync(a.top, 0x80, (size_t)OPN * a.B * a.Hkv * 4, s) != cudaSuccess) return ICT_ERR_CUDA;
+    const dim3 grid(bg, (unsigned)host::cdiv(L, kTopRows), (unsigned)a.n_op);
+    attn_top_kernel<<<grid, 256, 0, s>>>(a);
+    attn_copy_kernel<NV><<<grid, 256, 0, s>>>(a);
     host::counted(2);
     return host::launch_status();
 }
@@ -313,7 +363,7 @@ int32_t ict_attention_fwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     if (rows == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;
     host::Timer kt(s, ICT_KC_GEMM, 4.0 * (double)rows * a.Lk * a.D);
-    if ((st = align_operands(a, s))) return st;
+    if ((st = a.Dp == 64 ? align_operands<4>(a, s) : align_operands<8>(a, s))) return st;
     return a.Dp == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
 }
 
@@ -344,7 +394,7 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t rows = rq * a.Hq;
     host::Timer kt(s, ICT_KC_GEMM, 10.0 * (double)rows * a.Lk * a.D);
-    if ((st = align_operands(a, s))) return st;
+    if ((st = a.Dp == 64 ? align_operands<4>(a, s) : align_operands<8>(a, s))) return st;
     return a.Dp == 64 ? launch_bwd<64>(a, s) : launch_bwd<128>(a, s);
 }
 

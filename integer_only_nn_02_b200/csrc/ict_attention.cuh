@@ -17,7 +17,7 @@ enum { OPQ = 0, OPK = 1, OPV = 2, OPD = 3, OPN = 4 };  // operands: Q, K, V, dO
 struct AttnOperand {
     const int8_t *mant, *exp;
     int64_t ld;
-    int ngc, gv;      // groups per row, 16-column vectors per group
+    int ngc, gv, gsh; // groups per row, 16-column vectors per group, their shift (-1: not a power of two)
     int col, heads, L;
     const int32_t *lens;
     int8_t *copy;     // aligned copy [B][heads][L][Dp]

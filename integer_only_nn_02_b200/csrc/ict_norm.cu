@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(256) norm_fit_kernel(const __grid_constant__ N
 struct ValuesArgs {
     const int8_t *m, *e;
     int64_t rows, cols, ld, ldo, ngc;
-    int g_rows, g_cols;
+    int g_rows, g_cols, gsh;  // gsh: log2 of g_cols, or -1
     void *out;
 };
 __device__ __forceinline__ float ce_value(int C, int e) {  // C 2^e, in two exact steps
@@ -598,37 +598,54 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-// A thread writes 16 bytes of the output, so that stores are whole lines.
+// VEC: 16 columns per thread and step, four steps' loads in flight.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(256) values_kernel(const __grid_constant__ ValuesArgs a) {
-    constexpr int W = VEC ? (BF16 ? 8 : 4) : 1;
-    const int64_t per = a.cols / W, n = a.rows * per;
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < n; t += (int64_t)gridDim.x * 256) {
-        const int64_t i = t < (1ll << 31) && per < (1ll << 31) ? (int64_t)((uint32_t)t / (uint32_t)per) : t / per;
-        const int64_t j = (t - i * per) * W;
-        const int64_t gr = a.g_rows == 1 ? i : i / a.g_rows;
-        const int e = a.e[gr * a.ngc + (int)j / a.g_cols];
-        const int8_t *m = a.m + i * a.ld + j;
-        if constexpr (VEC) {
-            float v[W];
-            const int h = e == kEZero ? 0 : e / 2;
-            const float s0 = e == kEZero ? 0.0f : pow2f(h), s1 = e == kEZero ? 0.0f : pow2f(e - h);
-            if constexpr (BF16) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(m);
+    constexpr int W = VEC ? 16 : 1, U = VEC ? 4 : 1;
+    const uint32_t per = (uint32_t)(a.cols / W);
+    const int64_t n = a.rows * (int64_t)per, step = (int64_t)gridDim.x * 256;
+    for (int64_t t0 = (int64_t)blockIdx.x * 256 + threadIdx.x; t0 < n; t0 += U * step) {
+        uint4 w[U];
+        int e[U];
+        int64_t at[U];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = sx8f((q < 4 ? w.x : w.y) ^ 0x80808080u, q & 3) * s0 * s1;
-                *reinterpret_cast<uint4 *>((uint16_t *)a.out + i * a.ldo + j) =
-                    make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + u * step;
+            at[u] = -1;
+            if (t >= n) continue;
+            const int64_t i = n <= 0xffffffffll ? (int64_t)((uint32_t)t / per) : t / per;
+            const int j = (int)(t - i * per) * W;
+            const int64_t gr = a.g_rows == 1 ? i : i / a.g_rows;
+            e[u] = a.e[gr * a.ngc + (a.gsh >= 0 ? j >> a.gsh : j / a.g_cols)];
+            at[u] = i * a.ldo + j;
+            const int8_t *m = a.m + i * a.ld + j;
+            if constexpr (VEC) w[u] = *reinterpret_cast<const uint4 *>(m);
+            else w[u].x = (uint32_t)(uint8_t)*m;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (at[u] < 0) continue;
+            if constexpr (VEC) {
+                // 2^e in two exact factors
+                const int h = e[u] == kEZero ? 0 : e[u] / 2;
+                const float s0 = e[u] == kEZero ? 0.0f : pow2f(h), s1 = e[u] == kEZero ? 0.0f : pow2f(e[u] - h);
+                const uint32_t b[4] = {w[u].x ^ 0x80808080u, w[u].y ^ 0x80808080u, w[u].z ^ 0x80808080u, w[u].w ^ 0x80808080u};
+#pragma unroll
+                for (int q = 0; q < 4; q += BF16 ? 2 : 1) {
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < (BF16 ? 8 : 4); ++k) v[k] = sx8f(b[q + (k >> 2)], k & 3) * s0 * s1;
+                    if constexpr (BF16)
+                        *reinterpret_cast<uint4 *>((uint16_t *)a.out + at[u] + 4 * q) =
+                            make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+                    else
+                        *reinterpret_cast<float4 *>((float *)a.out + at[u] + 4 * q) = make_float4(v[0], v[1], v[2], v[3]);
+                }
             } else {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(m);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = sx8f(w ^ 0x80808080u, q) * s0 * s1;
-                *reinterpret_cast<float4 *>((float *)a.out + i * a.ldo + j) = make_float4(v[0], v[1], v[2], v[3]);
+                const float v = ce_value((int)(int8_t)w[u].x, e[u]);
+                if constexpr (BF16) ((uint16_t *)a.out)[at[u]] = (uint16_t)bf16x2(v, 0.0f);
+                else ((float *)a.out)[at[u]] = v;
             }
-        } else {
-            const float v = ce_value(*m, e);
-            if constexpr (BF16) ((uint16_t *)a.out)[i * a.ldo + j] = (uint16_t)bf16x2(v, 0.0f);
-            else ((float *)a.out)[i * a.ldo + j] = v;
         }
     }
 }
@@ -821,11 +838,12 @@ int32_t ict_values(const ict_tensor *t, int32_t bf16, void *out, int64_t ld_out,
     memset(&a, 0, sizeof(a));
     a.m = t->mant, a.e = t->exp, a.rows = t->rows, a.cols = t->cols, a.ld = t->ld, a.ldo = ld_out;
     a.g_rows = (int)std::min<int64_t>(t->g_rows, t->rows), a.g_cols = (int)std::min<int64_t>(t->g_cols, t->cols);
+    a.gsh = (a.g_cols & (a.g_cols - 1)) == 0 ? __builtin_ctz((unsigned)a.g_cols) : -1;
     a.ngc = groups_per_row(t);
     a.out = out;
     const bool vec = host::check_vec(t) == ICT_OK && (uintptr_t)out % 16 == 0 && ld_out % 8 == 0;
-    const int64_t n = t->rows * t->cols / (vec ? (bf16 ? 8 : 4) : 1);
-    const unsigned grid = (unsigned)std::min<int64_t>(host::cdiv(n, 256), 148 * 32);
+    const int64_t n = t->rows * t->cols / (vec ? 16 : 1);
+    const unsigned grid = (unsigned)std::min<int64_t>(host::cdiv(n, 256), 148 * 8);
     cudaStream_t s = (cudaStream_t)stream;
     host::Timer kt(s, ICT_KC_OTHER, (double)t->rows * t->cols * (bf16 ? 3 : 5));
     if (vec && bf16) values_kernel<true, true><<<grid, 256, 0, s>>>(a);

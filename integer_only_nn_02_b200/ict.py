@@ -140,8 +140,10 @@ def _check(code: int, what: str) -> None:
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the handle alone: building a torch.cuda.Stream for it takes microseconds of every call
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _ptr(t: torch.Tensor | None):
