@@ -6,6 +6,7 @@
 
 #include "ict_attention.cuh"
 #include "ict_attention_bwd.cuh"
+#include "ict_attention_few.cuh"
 #include "ict_attention_fwd.cuh"
 #include "ict_host.h"
 
@@ -92,8 +93,42 @@ template <int NV>
 __global__ void __launch_bounds__(512) attn_align_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ int m;
     const AttnOperand &o = a.op[blockIdx.y];
-    const int bg = blockIdx.x, b = bg / a.Hkv, n = clamp_len(o.lens, b, o.L);
-    const OperandRows r{o, b, bg - b * a.Hkv, o.heads / a.Hkv, 0, n, a.D / 16};
+    const int bg = blockIdx.x, b = bg / a.Hkv, n = clamp_len(o.lens, b, o.L), per = o.heads / a.Hkv;
+    const OperandRows r{o, b, bg - b * a.Hkv, per, 0, n, a.D / 16};
+    constexpr int U = 4;
+    const int rows = per * o.L;
+    if (rows * NV <= U * 512) {  // the vectors wait in registers for the block's largest exponent
+        uint4 w[U];
+        int e[U], mx = kNoExp;
+        if (threadIdx.x == 0) m = kNoExp;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = threadIdx.x + u * 512, rw = t / NV, v = t % NV, k = per == 1 ? 0 : rw / o.L, l = rw - k * o.L;
+            w[u] = make_uint4(0, 0, 0, 0);
+            e[u] = kEZero;
+            if (rw < rows && l < n && v < r.nvd) {
+                const int h = r.g * per + k;
+                w[u] = *reinterpret_cast<const uint4 *>(o.mant + ((int64_t)b * o.L + l) * o.ld + o.col + h * a.D + v * 16);
+                e[u] = r.exponent(l, h, v);
+                if (e[u] != kEZero) mx = max(mx, e[u]);
+            }
+        }
+        mx = warp_max(mx);
+        if ((threadIdx.x & 31) == 0 && mx > kNoExp) atomicMax(&m, mx);
+        __syncthreads();
+        const int es = m;
+        int8_t *dst = o.copy + ((int64_t)b * o.heads + r.g * per) * o.L * a.Dp;  // the group's heads lie one after the other
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = threadIdx.x + u * 512;
+            if (t >= rows * NV) continue;
+            if (e[u] != es) w[u] = rne_shift16(w[u], rne_index(es, e[u]));
+            *reinterpret_cast<uint4 *>(dst + (int64_t)t * 16) = w[u];
+        }
+        if (threadIdx.x == 0) a.top[blockIdx.y * a.B * a.Hkv + bg] = es;
+        return;
+    }
     const int es = block_top(r, &m);
     copy_rows<NV>(a, r, o.L, es);
     if (threadIdx.x == 0) a.top[blockIdx.y * a.B * a.Hkv + bg] = es;
@@ -178,6 +213,7 @@ int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
         d->len_k > 65536 || d->len_q > 65536)
         return ICT_ERR_LAYOUT;
     // 32-bit sums over all the queries of a key/value head
+    if ((int64_t)d->batch * d->heads_q * host::cdiv(std::max(d->len_q, d->len_k), 128) > 0x7fffffff) return ICT_ERR_LAYOUT;
     if (back && (int64_t)d->len_q * (d->heads_q / d->heads_kv) > 65536) return ICT_ERR_LAYOUT;
     memset(&a, 0, sizeof(a));
     a.B = d->batch, a.Hq = d->heads_q, a.Hkv = d->heads_kv, a.rep = a.Hq / a.Hkv, a.Lq = d->len_q, a.Lk = d->len_k;
@@ -187,11 +223,20 @@ int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
     return ICT_OK;
 }
 
+// A few queries per key/value head over many keys take the kernels that read K and V in place: at
+// 16 sequences of up to 16384 keys (4 heads of 64, 3 queries each) 369 us with the tensor-core
+// kernel become the figure beside few_values_kernel's description; below kFewKeys keys, or with
+// more queries (K and V are read once per kFewQ of them), the tiles win.
+bool few_queries_path(const AttnArgs &a, bool back) {
+    return !back && (int64_t)a.rep * a.Lq <= 2 * kFewQ && a.Lk >= kFewKeys;
+}
+
 struct Scratch {
     size_t top, copy[OPN], row, tmax, total;
+    size_t scores, mx, sum, acc;  // the few-queries path (scores apart, the others cleared before use)
 };
 Scratch scratch(const AttnArgs &a, bool back) {
-    Scratch s;
+    Scratch s = {};
     size_t at = 0;
     auto take = [&](int64_t bytes) {
         const size_t p = at;
@@ -200,6 +245,15 @@ Scratch scratch(const AttnArgs &a, bool back) {
     };
     const int64_t q = (int64_t)a.B * a.Hq * a.Lq, k = (int64_t)a.B * a.Hkv * a.Lk;
     s.top = take((int64_t)OPN * a.B * a.Hkv * 4);
+    if (few_queries_path(a, back)) {
+        const int64_t n = (int64_t)a.B * a.Hq * a.Lq;
+        s.mx = take(n * 4);
+        s.sum = take(n * 4);
+        s.acc = take(n * a.Dp * 8);
+        s.scores = take(n * a.Lk * 4);
+        s.total = at;
+        return s;
+    }
     s.copy[OPQ] = take(q * a.Dp);
     s.copy[OPK] = take(k * a.Dp);
     s.copy[OPV] = take(k * a.Dp);
@@ -268,6 +322,15 @@ int copy_map(CUtensorMap *m, const AttnArgs &a, int op) {
                          64, 128, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+// Blocks of a persistent kernel: as many as run at once, unless an item is long: then one per
+// item, which the hardware hands out as blocks finish (2 x 12 causal heads of 4096: 114 us against
+// 129 us with a fixed share of unequal items per block; 197 tokens: 65 us against 55 us).
+unsigned blocks_for(int64_t items, int per_sm, int len) {
+    int sms = 148;
+    host::device_info(&sms);
+    return (unsigned)(len > 512 ? items : std::min<int64_t>(items, (int64_t)sms * per_sm));
+}
+
 template <int DP>
 int launch_fwd(const AttnArgs &a, cudaStream_t s) {
     using L = FwdCfg<DP>;
@@ -278,10 +341,8 @@ int launch_fwd(const AttnArgs &a, cudaStream_t s) {
         return ICT_ERR_CUDA;
     AttnLimits lim;
     host::wait_limits(&lim.wait_ns, &lim.drain_ns);
-    int sms = 0;
-    if ((st = host::device_info(&sms))) return st;
     const int64_t items = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
-    const unsigned blocks = (unsigned)std::min<int64_t>(items, (int64_t)sms * (DP == 64 ? 2 : 1));
+    const unsigned blocks = blocks_for(items, DP == 64 ? 2 : 1, a.Lk);
     attn_fwd_kernel<DP><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, a, lim, (int)items);
     host::counted(1);
     return host::launch_status();
@@ -290,6 +351,29 @@ int launch_fwd(const AttnArgs &a, cudaStream_t s) {
 template <typename K>
 int allow_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? ICT_OK : ICT_ERR_CUDA;
+}
+
+template <int NV>
+int launch_few(const AttnArgs &a, const Scratch &w, cudaStream_t s) {
+    FewArgs p;
+    p.a = a;
+    p.R = a.rep * a.Lq;
+    uint8_t *base = (uint8_t *)a.top - w.top;
+    p.top = a.top;
+    p.mx = (int32_t *)(base + w.mx);
+    p.sum = (int32_t *)(base + w.sum);
+    p.acc = (unsigned long long *)(base + w.acc);
+    p.scores = (int32_t *)(base + w.scores);
+    // the exponents, maxima and sums lie before the scores
+    if (cudaMemsetAsync(p.top, 0, w.scores - w.top, s) != cudaSuccess) return ICT_ERR_CUDA;
+    const unsigned chunks = (unsigned)host::cdiv(a.Lk, kFewKeys), bg = (unsigned)(a.B * a.Hkv);
+    const unsigned qs = (unsigned)host::cdiv(p.R, kFewQ);
+    few_top_kernel<<<dim3((unsigned)a.B, chunks, 2), 256, 0, s>>>(p);
+    few_scores_kernel<NV><<<dim3(bg, chunks, qs), 256, 0, s>>>(p);
+    few_values_kernel<NV><<<dim3(bg, chunks, qs), 128, 0, s>>>(p);
+    few_out_kernel<<<(unsigned)host::cdiv((int64_t)bg * p.R, 8), 256, 0, s>>>(p);
+    host::counted(4);
+    return host::launch_status();
 }
 
 template <int DP>
@@ -306,20 +390,22 @@ int launch_bwd(const AttnArgs &a, cudaStream_t s) {
         constexpr int NL = DP / 16;
         attn_row_kernel<NL><<<(unsigned)host::cdiv(rows, 256 / NL), 256, 0, s>>>(a);
         if ((st = allow_smem(attn_dq_kernel<DP>, L::kBytes))) return st;
-        attn_dq_kernel<DP><<<(unsigned)(host::cdiv(a.Lq, kQTile) * a.B * a.Hq), L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+        const int64_t items = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
+        attn_dq_kernel<DP><<<blocks_for(items, 1, a.Lk), L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
         host::counted(2);
     }
     if ((int64_t)a.B * a.Lk > 0) {
         using L = DkvCfg<DP>;
-        const unsigned blocks = (unsigned)(host::cdiv(a.Lk, kKeyBlock) * a.B * a.Hkv);
+        const int64_t items = host::cdiv(a.Lk, kKeyBlock) * a.B * a.Hkv;
+        const unsigned blocks = blocks_for(items, 1, a.Lq * a.rep);
         if constexpr (DP == 64) {
             if ((st = allow_smem(attn_dkv_kernel<64, 3>, L::kBytes))) return st;
-            attn_dkv_kernel<64, 3><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+            attn_dkv_kernel<64, 3><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
             host::counted(1);
         } else {
             if ((st = allow_smem(attn_dkv_kernel<DP, 1>, L::kBytes)) || (st = allow_smem(attn_dkv_kernel<DP, 2>, L::kBytes))) return st;
-            attn_dkv_kernel<DP, 2><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
-            attn_dkv_kernel<DP, 1><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim);
+            attn_dkv_kernel<DP, 2><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
+            attn_dkv_kernel<DP, 1><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
             host::counted(2);
         }
     }
@@ -363,6 +449,7 @@ int32_t ict_attention_fwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     if (rows == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;
     host::Timer kt(s, ICT_KC_GEMM, 4.0 * (double)rows * a.Lk * a.D);
+    if (few_queries_path(a, false)) return a.Dp == 64 ? launch_few<4>(a, w, s) : launch_few<8>(a, w, s);
     if ((st = a.Dp == 64 ? align_operands<4>(a, s) : align_operands<8>(a, s))) return st;
     return a.Dp == 64 ? launch_fwd<64>(a, s) : launch_fwd<128>(a, s);
 }

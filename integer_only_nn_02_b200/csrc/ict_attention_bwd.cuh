@@ -86,73 +86,51 @@ __device__ __forceinline__ void dkv16(const uint32_t (&vs)[16], const uint32_t (
 
 template <int DP>
 struct DqCfg {
-    static constexpr int H = DP / 64, kTile = H * kHalfTile, KS = 3, VS = 2;
-    static constexpr int kOffD = kTile, kOffK = 2 * kTile, kOffV = kOffK + KS * kTile;
+    static constexpr int H = DP / 64, kTile = H * kHalfTile, QS = 2, KS = 3, VS = 2;
+    static constexpr int kOffK = QS * 2 * kTile, kOffV = kOffK + KS * kTile;  // Q stage: Q tile, dO tile
     static constexpr int kOffRed = kOffV + VS * kTile;  // [8][128] float2, [4][128] int
     static constexpr int kOffBar = kOffRed + 8 * 128 * 8 + 4 * 128 * 4;
-    static constexpr int kBars = 1 + 2 * KS + 2 * VS + 2 + 2 + 3;
+    static constexpr int kBars = 2 * (QS + KS + VS) + 2 + 2 + 4;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 64;
 };
 
+// Persistent blocks, as the forward's.
 template <int DP>
 __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmD,
-                   const __grid_constant__ AttnArgs a, const __grid_constant__ AttnLimits lim) {
+                   const __grid_constant__ AttnArgs a, const __grid_constant__ AttnLimits lim, int items) {
     using L = DqCfg<DP>;
-    constexpr int H = L::H;
+    constexpr int H = L::H, NS = 32 * kSoftWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(smem);
-    const uint32_t bar_q = sb + L::kOffBar;
-    const uint32_t bar_kf = bar_q + 8, bar_ke = bar_kf + 8 * L::KS;
+    const uint32_t bar_qf = sb + L::kOffBar, bar_qe = bar_qf + 8 * L::QS;
+    const uint32_t bar_kf = bar_qe + 8 * L::QS, bar_ke = bar_kf + 8 * L::KS;
     const uint32_t bar_vf = bar_ke + 8 * L::KS, bar_ve = bar_vf + 8 * L::VS;
-    const uint32_t bar_sf = bar_ve + 8 * L::VS, bar_ef = bar_sf + 16, bar_ee = bar_ef + 16;
-    const uint32_t bar_of = bar_ee + 8, bar_dr = bar_of + 8;
+    const uint32_t bar_sf = bar_ve + 8 * L::VS, bar_ef = bar_sf + 16;  // scores full, T written (per buffer)
+    const uint32_t bar_ee = bar_ef + 16, bar_of = bar_ee + 8, bar_oe = bar_of + 8, bar_dr = bar_oe + 8;
     volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);
     volatile int *abort_flag = &misc[1];
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-
-    const int ntq = (a.Lq + kQTile - 1) / kQTile, heads = a.B * a.Hq;
-    const int tile = ntq - 1 - (int)blockIdx.x / heads, bh = (int)blockIdx.x % heads;
-    const int b = bh / a.Hq, h = bh % a.Hq, g = h / a.rep, i0 = tile * kQTile;
-    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk);
-    const int last = min(nq, i0 + kQTile) - 1;
-    const int most = last < i0 ? 0 : (a.causal ? max(0, min(nk, last + nk - nq + 1)) : nk);
-    const int nt = (most + 127) / 128, nu = (most + kStep - 1) / kStep;
-    const int qrow = bh * a.Lq + i0, krow = (b * a.Hkv + g) * a.Lk;
-    auto load_tile = [&](const CUtensorMap *m, uint32_t dst, uint32_t bar, int row) {
-        for (int x = 0; x < H; ++x) tma_load_2d(dst + x * kHalfTile, m, bar, 64 * x, row);
-    };
-    if (threadIdx.x == 32 * kSoftWarps) {
+    if (threadIdx.x == NS) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
         prefetch_tmap(&tmD);
-        mbar_init(bar_q, 1);
+        for (int s = 0; s < L::QS; ++s) mbar_init(bar_qf + 8 * s, 1), mbar_init(bar_qe + 8 * s, 1);
         for (int s = 0; s < L::KS; ++s) mbar_init(bar_kf + 8 * s, 1), mbar_init(bar_ke + 8 * s, 1);
         for (int s = 0; s < L::VS; ++s) mbar_init(bar_vf + 8 * s, 1), mbar_init(bar_ve + 8 * s, 1);
         for (int s = 0; s < 2; ++s) mbar_init(bar_sf + 8 * s, 1), mbar_init(bar_ef + 8 * s, kSoftWarps / 2);
         mbar_init(bar_ee, 1);
         mbar_init(bar_of, 1);
+        mbar_init(bar_oe, kSoftWarps);
         mbar_init(bar_dr, 1);
         misc[1] = 0;
         fence_barrier_init();
-        if (nt > 0) {
-            mbar_expect_tx(bar_q, 2 * L::kTile);
-            load_tile(&tmQ, sb, bar_q, qrow);
-            load_tile(&tmD, sb + L::kOffD, bar_q, qrow);
-        }
     }
-    if (warp == kSoftWarps + 1) {
-        tmem_alloc(smem_u32((const void *)&misc[0]), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
     __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
     auto fail = [&]() {
         *abort_flag = 1;
         raise_status(ICT_ERR_DEVICE_TIMEOUT);
@@ -160,43 +138,75 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
 
     if (warp == kSoftWarps) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0 && nt > 0) {
+        if (lane == 0) {
+            auto load_tile = [&](const CUtensorMap *m, uint32_t dst, uint32_t bar, int row) {
+                for (int x = 0; x < H; ++x) tma_load_2d(dst + x * kHalfTile, m, bar, 64 * x, row);
+            };
+            auto free = [&](uint32_t bar, int n, int stages) {  // the n-th use of a ring's stage
+                return n < stages || wait_bar(bar + 8 * (n % stages), (n / stages - 1) & 1, lim.wait_ns, abort_flag);
+            };
             bool ok = true;
-            int n = 0;
-            for (int t = 0; t < nt; ++t) {
-                const int s = t % L::KS, v = t % L::VS;
-                if (t >= L::KS && !wait_bar(bar_ke + 8 * s, (t / L::KS - 1) & 1, lim.wait_ns, abort_flag)) ok = false;
-                if (ok && t >= L::VS && !wait_bar(bar_ve + 8 * v, (t / L::VS - 1) & 1, lim.wait_ns, abort_flag)) ok = false;
-                if (!ok) break;
-                mbar_expect_tx(bar_kf + 8 * s, L::kTile);
-                load_tile(&tmK, sb + L::kOffK + s * L::kTile, bar_kf + 8 * s, krow + t * 128);
-                mbar_expect_tx(bar_vf + 8 * v, L::kTile);
-                load_tile(&tmV, sb + L::kOffV + v * L::kTile, bar_vf + 8 * v, krow + t * 128);
-                ++n;
+            int qn = 0, kn = 0, vn = 0;
+            for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+                const AttnItem w = attn_item(a, item);
+                if (w.nt == 0) continue;
+                if (!(ok = free(bar_qe, qn, L::QS))) break;
+                const uint32_t dst = sb + (qn % L::QS) * 2 * L::kTile, bar = bar_qf + 8 * (qn % L::QS);
+                mbar_expect_tx(bar, 2 * L::kTile);
+                load_tile(&tmQ, dst, bar, w.bh * a.Lq + w.i0);
+                load_tile(&tmD, dst + L::kTile, bar, w.bh * a.Lq + w.i0);
+                ++qn;
+                const int krow = (w.b * a.Hkv + w.g) * a.Lk;
+                for (int t = 0; t < w.nt; ++t) {
+                    if (!(ok = free(bar_ke, kn, L::KS))) break;
+                    mbar_expect_tx(bar_kf + 8 * (kn % L::KS), L::kTile);
+                    load_tile(&tmK, sb + L::kOffK + (kn % L::KS) * L::kTile, bar_kf + 8 * (kn % L::KS), krow + t * 128);
+                    ++kn;
+                    if (!(ok = free(bar_ve, vn, L::VS))) break;
+                    mbar_expect_tx(bar_vf + 8 * (vn % L::VS), L::kTile);
+                    load_tile(&tmV, sb + L::kOffV + (vn % L::VS) * L::kTile, bar_vf + 8 * (vn % L::VS), krow + t * 128);
+                    ++vn;
+                }
             }
             if (!ok) fail();
-            wait_bar(bar_q, 0, lim.drain_ns, nullptr);
-            for (int t = max(0, n - L::KS); t < n; ++t)
-                wait_bar(bar_kf + 8 * (t % L::KS), (t / L::KS) & 1, lim.drain_ns, nullptr);
-            for (int t = max(0, n - L::VS); t < n; ++t)
-                wait_bar(bar_vf + 8 * (t % L::VS), (t / L::VS) & 1, lim.drain_ns, nullptr);
+            // every copy lands before the block may end
+            for (int k = max(0, qn - L::QS); k < qn; ++k)
+                wait_bar(bar_qf + 8 * (k % L::QS), (k / L::QS) & 1, lim.drain_ns, nullptr);
+            for (int k = max(0, kn - L::KS); k < kn; ++k)
+                wait_bar(bar_kf + 8 * (k % L::KS), (k / L::KS) & 1, lim.drain_ns, nullptr);
+            for (int k = max(0, vn - L::VS); k < vn; ++k)
+                wait_bar(bar_vf + 8 * (k % L::VS), (k / L::VS) & 1, lim.drain_ns, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (nt > 0) {
-            constexpr uint32_t kIdS = idesc_i8(128, kStep);
-            constexpr uint32_t kIdHi = idesc_i8(128, DP, false, true);              // signed high plane
-            constexpr uint32_t kIdLo = idesc_i8(128, DP, false, true) & ~(1u << 7);  // unsigned low plane
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                return (bool)__all_sync(0xffffffffu, wait_bar(bar, parity, lim.wait_ns, abort_flag));
-            };
-            bool ok = wait(bar_q, 0);
+        // ------------------------------------------------------------ TMEM and MMA issue
+        tmem_alloc(smem_u32((const void *)&misc[0]), 512);
+        tmem_relinquish();
+        tc_fence_before();
+        named_bar_sync(2, NS + 32);
+        tc_fence_after();
+        const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
+        constexpr uint32_t kIdS = idesc_i8(128, kStep);
+        constexpr uint32_t kIdHi = idesc_i8(128, DP, false, true);              // signed high plane
+        constexpr uint32_t kIdLo = idesc_i8(128, DP, false, true) & ~(1u << 7);  // unsigned low plane
+        auto wait = [&](uint32_t bar, int parity) {
+            return (bool)__all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(parity & 1), lim.wait_ns, abort_flag));
+        };
+        bool ok = true;
+        int qn = 0, kn = 0, k0 = 0, vn = 0, pn = 0, on = 0;  // kn: K tiles whose scores, k0: whose products are done
+        uint32_t ef_par = 0;
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            const AttnItem w = attn_item(a, item);
+            if (w.nt == 0) continue;
+            const int nu = (w.most + kStep - 1) / kStep;
+            const uint32_t qt = sb + (qn % L::QS) * 2 * L::kTile;
+            if (!(ok = wait(bar_qf + 8 * (qn % L::QS), qn / L::QS))) break;
             // S and dP of step u into buffer u & 1
             auto scores = [&](int u) {
-                const int t = u >> 1, s = t % L::KS, v = t % L::VS, half = u & 1;
-                if (half == 0 && (!wait(bar_kf + 8 * s, (t / L::KS) & 1) || !wait(bar_vf + 8 * v, (t / L::VS) & 1))) return false;
+                const int s = kn % L::KS, v = vn % L::VS, half = u & 1;
+                if (half == 0 && (!wait(bar_kf + 8 * s, kn / L::KS) || !wait(bar_vf + 8 * v, vn / L::VS))) return false;
                 tc_fence_after();
-                const uint64_t dq = smem_desc_kmajor(sb, 64), dd = smem_desc_kmajor(sb + L::kOffD, 64);
+                const bool done = half == 1 || u + 1 == nu;
+                const uint64_t dq = smem_desc_kmajor(qt, 64), dd = smem_desc_kmajor(qt + L::kTile, 64);
                 const uint64_t dk = smem_desc_kmajor(sb + L::kOffK + s * L::kTile + half * kStep * 64, 64);
                 const uint64_t dv = smem_desc_kmajor(sb + L::kOffV + v * L::kTile + half * kStep * 64, 64);
                 const uint32_t col = tm + (u & 1) * 128;
@@ -211,23 +221,30 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
                         const int o = (x >> 1) * (kHalfTile >> 4) + 2 * (x & 1);
                         umma_i8(col + kStep, dd + o, dv + o, kIdS, x ? 1u : 0u);
                     }
-                    if (half == 1 || u + 1 == nu) umma_commit(bar_ve + 8 * v);
+                    if (done) umma_commit(bar_ve + 8 * v);
+                    if (u + 1 == nu) umma_commit(bar_qe + 8 * (qn % L::QS));
                     umma_commit(bar_sf + 8 * (u & 1));
                 }
                 __syncwarp();
+                if (done) ++kn, ++vn;
                 return true;
             };
-            if (ok) ok = scores(0);
+            // the last item's T planes are used; its dQ is read before this item's first product
+            if (pn > 0 && !(ok = wait(bar_ee, pn - 1))) break;
+            ok = scores(0);
             for (int u = 0; u < nu && ok; ++u) {
                 if (u + 1 < nu) {
-                    if (u > 0) ok = wait(bar_ee, (u - 1) & 1);
+                    if (u > 0) ok = wait(bar_ee, pn - 1);
                     if (!ok || !(ok = scores(u + 1))) break;
                 }
-                if (!(ok = wait(bar_ef + 8 * (u & 1), (u >> 1) & 1))) break;
+                if (!(ok = wait(bar_ef + 8 * (u & 1), (ef_par >> (u & 1)) & 1))) break;
+                ef_par ^= 1u << (u & 1);
+                if (u == 0 && on > 0 && !(ok = wait(bar_oe, on - 1))) break;
                 tc_fence_after();
-                const int s = (u >> 1) % L::KS, ks = (min(kStep, most - u * kStep) + 31) / 32;
+                const int s = k0 % L::KS, ks = (min(kStep, w.most - u * kStep) + 31) / 32;
                 const uint64_t dk = smem_desc_mnmajor64(sb + L::kOffK + s * L::kTile + (u & 1) * kStep * 64, kHalfTile);
                 const uint32_t e0 = tm + (u & 1) * 128, first = u ? 1u : 0u;
+                const bool done = (u & 1) || u + 1 == nu;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk)
@@ -235,78 +252,93 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
                             umma_i8_ta(tm + kAccCol, e0 + kk * 32, dk + 128 * kk, kIdHi, kk ? 1u : first);
                             umma_i8_ta(tm + kAccCol + DP, e0 + kk * 32 + 8, dk + 128 * kk, kIdLo, kk ? 1u : first);
                         }
-                    if ((u & 1) || u + 1 == nu) umma_commit(bar_ke + 8 * s);
+                    if (done) umma_commit(bar_ke + 8 * s);
                     umma_commit(bar_ee);
+                    if (u + 1 == nu) umma_commit(bar_of);
                 }
                 __syncwarp();
+                ++pn;
+                if (done) ++k0;
             }
-            if (!ok && lane == 0) fail();
-            if (elect_one()) {
-                umma_commit(bar_of);
-                umma_commit(bar_dr);
-            }
-            __syncwarp();
-            wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
-        }
-    } else {
-        // ------------------------------------------------------------ softmax
-        const int wg = warp >> 2, et = threadIdx.x & 127, i = i0 + et, pair = wg >> 1, c0 = (wg & 1) * 32;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int see = i >= nq ? 0 : (a.causal ? max(0, min(nk, i + nk - nq + 1)) : nk);
-        const int see_max = warp_max(see), see_min = -warp_max(-see);
-        const bool live = i < a.Lq;
-        const int64_t at = (int64_t)bh * a.Lq + (live ? i : 0);
-        int2 st = make_int2(0, 0), rw = make_int2(0, 0);
-        if (live && nt > 0) st = a.stats[at], rw = a.row[at];
-        const int tau = 32 - __clz(rw.y), bg = b * a.Hkv + g;
-        const f2 nm = pk(-(kAttnMagic + (float)st.x)), nd = pk(-(kAttnMagic + (float)rw.x));
-        const f2 f = pk(attn_factor(a, bg)), sc = pk(pow2f(-tau));
-        int tmax = 0x4B400000, tmin = 0x4B400000;
-        bool ok = true;
-        for (int u = pair; u < nu && ok; u += 2) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, (u >> 1) & 1, lim.wait_ns, abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            const int col = u * kStep + c0;
-            if (c0 < most - u * kStep) {
-                const uint32_t mine = tm + lanes + pair * 128 + c0;
-#pragma unroll 1
-                for (int c = 0; c < 32; c += 16) {
-                    uint32_t lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
-                    if (col + c < see_max) {
-                        uint32_t vs[16], vd[16];
-                        tmem_ld16(mine + c, vs);
-                        tmem_ld16(mine + kStep + c, vd);
-                        tmem_ld_done(vs, vd);
-                        if (col + c + 16 <= see_min) dq16<false>(vs, vd, nm, nd, f, sc, 0, tmax, tmin, lo, hi);
-                        else dq16<true>(vs, vd, nm, nd, f, sc, see - col - c, tmax, tmin, lo, hi);
-                    }
-                    tmem_st4(mine + c / 4, hi);  // in the place of scores already read
-                    tmem_st4(mine + 8 + c / 4, lo);
-                }
-                tmem_st_wait();
-            }
-            warp_arrive(bar_ef + 8 * pair);
-        }
-        int *red = (int *)(smem + L::kOffRed + 8 * 128 * 8);
-        red[wg * 128 + et] = max(tmax - 0x4B400000, 0x4B400000 - tmin);
-        if (nt > 0 && ok) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar_of, 0, lim.wait_ns, abort_flag));
-            tc_fence_after();
+            ++qn;
+            ++on;
         }
         if (!ok && lane == 0) fail();
-        const bool read = nt > 0 && ok;
-        float2 *gm = (float2 *)(smem + L::kOffRed) + et;
-        const int cc = wg * (DP / 4);
-        fit_row_tmem<DP / 64>(a, a.o, (int64_t)b * a.Lq + i, h, cc, read ? st.y : 0, a.mul,
-                              tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
-                              nk <= 1024, gm, 128, 1, 32 * kSoftWarps, AccCols{tm + lanes + kAccCol, DP, read});
-        if (wg == 0 && live) a.tmax[at] = max(max(red[et], red[128 + et]), max(red[256 + et], red[384 + et]));
+        if (elect_one()) umma_commit(bar_dr);
+        __syncwarp();
+        wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
+    } else {
+        // ------------------------------------------------------------ softmax
+        named_bar_sync(2, NS + 32);
+        tc_fence_after();
+        const uint32_t tm = (uint32_t)misc[0];
+        const int wg = warp >> 2, et = threadIdx.x & 127, pair = wg >> 1, c0 = (wg & 1) * 32;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        int *red = (int *)(smem + L::kOffRed + 8 * 128 * 8);
+        bool ok = true;
+        int on = 0, sn = 0;  // outputs, this pair's steps so far
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {  // (outputs are written after a failure too)
+            const AttnItem w = attn_item(a, item);
+            const int i = w.i0 + et, nu = (w.most + kStep - 1) / kStep, bg = w.b * a.Hkv + w.g;
+            const int see = i >= w.nq ? 0 : (a.causal ? max(0, min(w.nk, i + w.nk - w.nq + 1)) : w.nk);
+            const int see_max = warp_max(see), see_min = -warp_max(-see);
+            const bool live = i < a.Lq;
+            const int64_t at = (int64_t)w.bh * a.Lq + (live ? i : 0);
+            int2 st = make_int2(0, 0), rw = make_int2(0, 0);
+            if (live && w.nt > 0) st = a.stats[at], rw = a.row[at];
+            const int tau = 32 - __clz(rw.y);
+            const f2 nm = pk(-(kAttnMagic + (float)st.x)), nd = pk(-(kAttnMagic + (float)rw.x));
+            const f2 f = pk(attn_factor(a, bg)), sc = pk(pow2f(-tau));
+            int tmax = 0x4B400000, tmin = 0x4B400000;
+            for (int u = pair; u < nu && ok; u += 2) {
+                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, sn & 1, lim.wait_ns, abort_flag));
+                if (!ok) break;
+                ++sn;
+                tc_fence_after();
+                const int col = u * kStep + c0;
+                if (c0 < w.most - u * kStep) {
+                    const uint32_t mine = tm + lanes + pair * 128 + c0;
+#pragma unroll 1
+                    for (int c = 0; c < 32; c += 16) {
+                        uint32_t lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
+                        if (col + c < see_max) {
+                            uint32_t vs[16], vd[16];
+                            tmem_ld16(mine + c, vs);
+                            tmem_ld16(mine + kStep + c, vd);
+                            tmem_ld_done(vs, vd);
+                            if (col + c + 16 <= see_min) dq16<false>(vs, vd, nm, nd, f, sc, 0, tmax, tmin, lo, hi);
+                            else dq16<true>(vs, vd, nm, nd, f, sc, see - col - c, tmax, tmin, lo, hi);
+                        }
+                        tmem_st4(mine + c / 4, hi);  // in the place of scores already read
+                        tmem_st4(mine + 8 + c / 4, lo);
+                    }
+                    tmem_st_wait();
+                }
+                warp_arrive(bar_ef + 8 * pair);
+            }
+            red[wg * 128 + et] = max(tmax - 0x4B400000, 0x4B400000 - tmin);
+            if (w.nt > 0 && ok) {
+                ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
+                tc_fence_after();
+            }
+            const bool read = w.nt > 0 && ok;
+            float2 *gm = (float2 *)(smem + L::kOffRed) + et;
+            fit_row_tmem<DP / 64>(a, a.o, (int64_t)w.b * a.Lq + i, w.h, wg * (DP / 4), read ? st.y : 0, a.mul,
+                                  tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
+                                  w.nk <= 1024, gm, 128, 1, NS, AccCols{tm + lanes + kAccCol, DP, read});
+            if (wg == 0 && live) a.tmax[at] = max(max(red[et], red[128 + et]), max(red[256 + et], red[384 + et]));
+            if (w.nt > 0) {
+                warp_arrive(bar_oe);
+                ++on;
+            }
+            named_bar_sync(1, NS);  // the shared maxima are read before the next item's are written
+        }
+        if (!ok && lane == 0) fail();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kSoftWarps + 1) tmem_dealloc(tm, 512);
+    if (warp == kSoftWarps + 1) tmem_dealloc(__shfl_sync(0xffffffffu, (uint32_t)misc[0], 0), 512);
 }
 
 // rn24(2^pi / rn24(S)) of a row; 0 for a row that sees no key
@@ -318,152 +350,198 @@ __device__ __forceinline__ int64_t attn_bound(float rho, int tmax, int X) {
 
 template <int DP>
 struct DkvCfg {
-    static constexpr int H = DP / 64, kTile = H * kHalfTile, QS = 2;
-    static constexpr int kOffV = kTile, kOffQ = 2 * kTile;                 // stage: Q tile, dO tile
+    static constexpr int H = DP / 64, kTile = H * kHalfTile, KS = 2, QS = 2;
+    static constexpr int kOffQ = KS * 2 * kTile;                           // K stage: K tile, V tile; Q stage: Q tile, dO tile
     static constexpr int kOffVec = kOffQ + QS * 2 * kTile;                 // [4][3][64] floats
     static constexpr int kOffRed = kOffVec + 4 * 3 * kStep * 4;            // [2][8][128] float2
     static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8;
-    static constexpr int kBars = 1 + 2 * QS + 2 + 2 + 4 + 4 + 3;
-    static constexpr int kBytes = kOffBar + kBars * 8 + 48 + 1024;
+    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 2 + 2 + 4;
+    static constexpr int kBytes = kOffBar + kBars * 8 + 64 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 96;
 };
 
-// MODE: 3 computes dV and dK (heads of 64 columns), 1 only dV, 2 only dK.
+// One work item: a block of keys of one key/value head.  Heavy causal blocks come first.
+struct KeyItem {
+    int b, g, bg, j0, nq, nk, off, i0, n, base, tiles, per, nw, nu;
+};
+__device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
+    KeyItem w;
+    const int heads = a.B * a.Hkv, J = item / heads;
+    w.bg = item - J * heads;
+    w.b = w.bg / a.Hkv;
+    w.g = w.bg - w.b * a.Hkv;
+    w.j0 = J * kKeyBlock;
+    w.nq = clamp_len(a.op[OPQ].lens, w.b, a.Lq);
+    w.nk = clamp_len(a.op[OPK].lens, w.b, a.Lk);
+    w.off = w.nk - w.nq;
+    w.i0 = a.causal ? max(0, w.j0 - w.off) : 0;          // first query that sees the block
+    w.n = w.j0 < w.nk ? max(0, w.nq - w.i0) : 0;         // such queries of one head
+    w.base = w.i0 & ~(kStep - 1);
+    w.tiles = w.n > 0 ? (w.nq - w.base + 127) / 128 : 0;
+    w.per = w.n > 0 ? (w.nq - w.base + kStep - 1) / kStep : 0;  // steps of one head
+    w.nw = w.tiles * a.rep;
+    w.nu = w.per * a.rep;
+    return w;
+}
+
+// MODE: 3 computes dV and dK (heads of 64 columns), 1 only dV, 2 only dK.  Persistent blocks.
 template <int DP, int MODE>
 __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
     attn_dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmD,
-                    const __grid_constant__ AttnArgs a, const __grid_constant__ AttnLimits lim) {
+                    const __grid_constant__ AttnArgs a, const __grid_constant__ AttnLimits lim, int items) {
     using L = DkvCfg<DP>;
-    constexpr int H = L::H;
+    constexpr int H = L::H, NS = 32 * kSoftWarps;
     static_assert(MODE != 3 || DP == 64, "both gradients: 256 accumulator columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t sb = smem_u32(smem);
-    const uint32_t bar_k = sb + L::kOffBar;
-    const uint32_t bar_qf = bar_k + 8, bar_qe = bar_qf + 8 * L::QS;
+    const uint32_t bar_kf = sb + L::kOffBar, bar_ke = bar_kf + 8 * L::KS;
+    const uint32_t bar_qf = bar_ke + 8 * L::KS, bar_qe = bar_qf + 8 * L::QS;
     const uint32_t bar_sf = bar_qe + 8 * L::QS, bar_ef = bar_sf + 16;
     const uint32_t bar_cf = bar_ef + 16, bar_ce = bar_cf + 32;  // the queries' vectors full / empty
-    const uint32_t bar_ee = bar_ce + 32, bar_of = bar_ee + 8, bar_dr = bar_of + 8;
-    volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);  // tmem, abort, min S, -, bound (64 bits)
+    const uint32_t bar_xf = bar_ce + 32, bar_xe = bar_xf + 16;  // an item's exponents full / empty
+    const uint32_t bar_ee = bar_xe + 16, bar_of = bar_ee + 8, bar_oe = bar_of + 8, bar_dr = bar_oe + 8;
+    // tmem, abort, -, -, [2] pi, c, [2] smallest sum, [2] largest bound (64 bits)
+    volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);
+    int *smin = (int *)(misc + 8);
+    unsigned long long *bmax = (unsigned long long *)(misc + 10);
     volatile int *abort_flag = &misc[1];
-    unsigned long long *wmax = (unsigned long long *)(smem + L::kOffBar + L::kBars * 8 + 16);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-
-    const int bg = (int)blockIdx.x % (a.B * a.Hkv), J = (int)blockIdx.x / (a.B * a.Hkv);  // heavy causal blocks first
-    const int b = bg / a.Hkv, g = bg % a.Hkv, j0 = J * kKeyBlock;
-    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk);
-    const int off = nk - nq;
-    const int i0 = a.causal ? max(0, j0 - off) : 0;             // first query that sees the block
-    const int n = j0 < nk ? max(0, nq - i0) : 0;                // such queries of one head
-    const int base = i0 & ~(kStep - 1), tiles = n > 0 ? (nq - base + 127) / 128 : 0;
-    const int per = n > 0 ? (nq - base + kStep - 1) / kStep : 0;  // steps of one head
-    const int nw = tiles * a.rep, nu = per * a.rep;
-    auto load_tile = [&](const CUtensorMap *m, uint32_t dst, uint32_t bar, int row) {
-        for (int x = 0; x < H; ++x) tma_load_2d(dst + x * kHalfTile, m, bar, 64 * x, row);
-    };
-    if (threadIdx.x == 32 * kSoftWarps) {
+    if (threadIdx.x == NS) {
         prefetch_tmap(&tmQ);
         prefetch_tmap(&tmK);
         prefetch_tmap(&tmV);
         prefetch_tmap(&tmD);
-        mbar_init(bar_k, 1);
+        for (int s = 0; s < L::KS; ++s) mbar_init(bar_kf + 8 * s, 1), mbar_init(bar_ke + 8 * s, 1);
         for (int s = 0; s < L::QS; ++s) mbar_init(bar_qf + 8 * s, 1), mbar_init(bar_qe + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) mbar_init(bar_sf + 8 * s, 1), mbar_init(bar_ef + 8 * s, kSoftWarps / 2);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar_sf + 8 * s, 1);
+            mbar_init(bar_ef + 8 * s, kSoftWarps / 2);
+            mbar_init(bar_xf + 8 * s, 1);
+            mbar_init(bar_xe + 8 * s, kSoftWarps);
+        }
         for (int s = 0; s < 4; ++s) mbar_init(bar_cf + 8 * s, 1), mbar_init(bar_ce + 8 * s, kSoftWarps / 2);
         mbar_init(bar_ee, 1);
         mbar_init(bar_of, 1);
+        mbar_init(bar_oe, kSoftWarps);
         mbar_init(bar_dr, 1);
         misc[1] = 0;
-        misc[2] = INT_MAX;
-        *wmax = 0;
+        smin[0] = smin[1] = INT_MAX;
+        bmax[0] = bmax[1] = 0;
         fence_barrier_init();
-        if (nu > 0) {
-            const int krow = bg * a.Lk + j0;
-            mbar_expect_tx(bar_k, 2 * L::kTile);
-            load_tile(&tmK, sb, bar_k, krow);
-            load_tile(&tmV, sb + L::kOffV, bar_k, krow);
-        }
-    }
-    if (warp == kSoftWarps + 1) {
-        tmem_alloc(smem_u32((const void *)&misc[0]), 512);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
-    // the block's exponents: pi from the smallest sum of weights, c from the largest bound
-    const int total = n * a.rep;
-    auto index = [&](int t) { return ((int64_t)b * a.Hq + g * a.rep + t / n) * a.Lq + i0 + t % n; };
-    {
-        int m = INT_MAX;
-        for (int t = threadIdx.x; t < total; t += L::kThreads) {
-            const int S = a.stats[index(t)].y;
-            if (S > 0) m = min(m, S);
-        }
-        m = -warp_max(-m);
-        if (lane == 0) atomicMin((int *)&misc[2], m);
     }
     __syncthreads();
-    const int pi = misc[2] == INT_MAX ? 0 : 31 - __clz(misc[2]);
-    if (MODE & 2) {
-        unsigned long long w = 0;
-        for (int t = threadIdx.x; t < total; t += L::kThreads) {
-            const int64_t at = index(t);
-            const int S = a.stats[at].y;
-            if (S > 0) w = max(w, (unsigned long long)attn_bound(attn_rho(S, pi), a.tmax[at], a.row[at].y));
-        }
-        for (int o = 16; o > 0; o >>= 1) w = max(w, __shfl_xor_sync(0xffffffffu, w, o));
-        if (lane == 0) atomicMax(wmax, w);
-    }
-    __syncthreads();
-    const int cexp = max(0, 64 - __clzll((long long)*wmax) - 14);
     auto fail = [&]() {
         *abort_flag = 1;
         raise_status(ICT_ERR_DEVICE_TIMEOUT);
     };
-    // step u: query head g rep + u / per, queries base + (u % per) 64 ...
+    // An item's exponents: pi from the smallest sum of weights, c from the largest bound, over the
+    // queries that see the block.  Few queries: the vector warp finds them, an item ahead.  Many:
+    // the softmax warps do, all their threads reading; both then meet at a barrier (slot ls of
+    // the two alternates; thread 0 clears the other one, whose readers have passed a barrier).
+    auto row_of = [&](const KeyItem &w, int t) {
+        const int r = t / w.n;
+        return ((int64_t)w.b * a.Hq + w.g * a.rep + r) * a.Lq + w.nq - w.n + (t - r * w.n);
+    };
+    auto is_long = [&](const KeyItem &w) { return w.n * a.rep > 512; };
+    auto long_exponents = [&](const KeyItem &w, int ls, int tid, int &pi, int &c) {  // tid < 0: only meet
+        const int total = w.n * a.rep;
+        if (tid >= 0) {
+            int m = INT_MAX;
+            for (int t = tid; t < total; t += NS) {
+                const int S = a.stats[row_of(w, t)].y;
+                m = S > 0 ? min(m, S) : m;
+            }
+            m = -warp_max(-m);
+            if (lane == 0) atomicMin(&smin[ls], m);
+        }
+        named_bar_sync(4, NS + 32);
+        const int m = *(volatile int *)&smin[ls];
+        pi = m == INT_MAX ? 0 : 31 - __clz(m);
+        if (tid == 0) smin[ls ^ 1] = INT_MAX, bmax[ls ^ 1] = 0;
+        if (tid >= 0 && (MODE & 2)) {
+            unsigned long long x = 0;
+            for (int t = tid; t < total; t += NS) {
+                const int64_t at = row_of(w, t);
+                const int S = a.stats[at].y;
+                if (S > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), a.tmax[at], a.row[at].y));
+            }
+            for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+            if (lane == 0) atomicMax(&bmax[ls], x);
+        }
+        named_bar_sync(4, NS + 32);
+        const unsigned long long x = *(volatile unsigned long long *)&bmax[ls];
+        c = max(0, 64 - __clzll((long long)x) - 14);
+    };
+    // step u of an item: query head g rep + u / per, queries base + (u % per) 64 ...
     if (warp == kSoftWarps) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0 && nu > 0) {
+        if (lane == 0) {
+            auto load_tile = [&](const CUtensorMap *m, uint32_t dst, uint32_t bar, int row) {
+                for (int x = 0; x < H; ++x) tma_load_2d(dst + x * kHalfTile, m, bar, 64 * x, row);
+            };
+            auto free = [&](uint32_t bar, int n, int stages) {
+                return n < stages || wait_bar(bar + 8 * (n % stages), (n / stages - 1) & 1, lim.wait_ns, abort_flag);
+            };
             bool ok = true;
-            int w = 0;
-            for (; w < nw; ++w) {
-                const int s = w % L::QS;
-                if (w >= L::QS && !wait_bar(bar_qe + 8 * s, (w / L::QS - 1) & 1, lim.wait_ns, abort_flag)) {
-                    ok = false;
-                    break;
+            int kn = 0, qn = 0;
+            for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+                const KeyItem w = key_item(a, item);
+                if (w.nu == 0) continue;
+                if (!(ok = free(bar_ke, kn, L::KS))) break;
+                const uint32_t dst = sb + (kn % L::KS) * 2 * L::kTile, bar = bar_kf + 8 * (kn % L::KS);
+                mbar_expect_tx(bar, 2 * L::kTile);
+                load_tile(&tmK, dst, bar, w.bg * a.Lk + w.j0);
+                load_tile(&tmV, dst + L::kTile, bar, w.bg * a.Lk + w.j0);
+                ++kn;
+                for (int t = 0; t < w.nw; ++t) {
+                    if (!(ok = free(bar_qe, qn, L::QS))) break;
+                    const int row = (w.b * a.Hq + w.g * a.rep + t / w.tiles) * a.Lq + w.base + (t % w.tiles) * 128;
+                    const uint32_t q = sb + L::kOffQ + (qn % L::QS) * 2 * L::kTile, bq = bar_qf + 8 * (qn % L::QS);
+                    mbar_expect_tx(bq, 2 * L::kTile);
+                    load_tile(&tmQ, q, bq, row);
+                    load_tile(&tmD, q + L::kTile, bq, row);
+                    ++qn;
                 }
-                const int row = (b * a.Hq + g * a.rep + w / tiles) * a.Lq + base + (w % tiles) * 128;
-                const uint32_t dst = sb + L::kOffQ + s * 2 * L::kTile;
-                mbar_expect_tx(bar_qf + 8 * s, 2 * L::kTile);
-                load_tile(&tmQ, dst, bar_qf + 8 * s, row);
-                load_tile(&tmD, dst + L::kTile, bar_qf + 8 * s, row);
             }
             if (!ok) fail();
-            wait_bar(bar_k, 0, lim.drain_ns, nullptr);
-            for (int t = max(0, w - L::QS); t < w; ++t)
+            for (int t = max(0, kn - L::KS); t < kn; ++t)
+                wait_bar(bar_kf + 8 * (t % L::KS), (t / L::KS) & 1, lim.drain_ns, nullptr);
+            for (int t = max(0, qn - L::QS); t < qn; ++t)
                 wait_bar(bar_qf + 8 * (t % L::QS), (t / L::QS) & 1, lim.drain_ns, nullptr);
         }
     } else if (warp == kSoftWarps + 1) {
-        // ------------------------------------------------------------ MMA issuer
-        if (nu > 0) {
-            constexpr uint32_t kIdS = idesc_i8(128, kStep);
-            constexpr uint32_t kIdHi = idesc_i8(128, DP, false, true);
-            constexpr uint32_t kIdLo = idesc_i8(128, DP, false, true) & ~(1u << 7);
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                return (bool)__all_sync(0xffffffffu, wait_bar(bar, parity, lim.wait_ns, abort_flag));
-            };
-            bool ok = wait(bar_k, 0);
-            // walk of the steps: tile index w and half within the tile, for the scores and for the products
-            int sw = 0, sh = 0, sk = 0, pw = 0, ph = 0, pk_ = 0;  // sk, pk_: step within the head
+        // ------------------------------------------------------------ TMEM and MMA issue
+        tmem_alloc(smem_u32((const void *)&misc[0]), 512);
+        tmem_relinquish();
+        tc_fence_before();
+        named_bar_sync(3, NS + 32);
+        tc_fence_after();
+        const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
+        constexpr uint32_t kIdS = idesc_i8(128, kStep);
+        constexpr uint32_t kIdHi = idesc_i8(128, DP, false, true);
+        constexpr uint32_t kIdLo = idesc_i8(128, DP, false, true) & ~(1u << 7);
+        constexpr int kDk = MODE == 3 ? kAccCol + 2 * DP : kAccCol;
+        auto wait = [&](uint32_t bar, int parity) {
+            return (bool)__all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(parity & 1), lim.wait_ns, abort_flag));
+        };
+        bool ok = true;
+        int kn = 0, pn = 0, on = 0, sw = 0, pw = 0;  // sw, pw: query tiles whose scores, products are done
+        uint32_t ef_par = 0;
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
+            const KeyItem w = key_item(a, item);
+            if (w.nu == 0) continue;
+            const uint32_t kt = sb + (kn % L::KS) * 2 * L::kTile;
+            if (!(ok = wait(bar_kf + 8 * (kn % L::KS), kn / L::KS))) break;
+            // half within the tile and step within the head, for the scores and for the products
+            int sh = 0, sk = 0, ph = 0, pk_ = 0;
             auto scores = [&](int u) {
                 const int s = sw % L::QS;
-                if (sh == 0 && !wait(bar_qf + 8 * s, (sw / L::QS) & 1)) return false;
+                if (sh == 0 && !wait(bar_qf + 8 * s, sw / L::QS)) return false;
                 tc_fence_after();
                 const uint32_t q = sb + L::kOffQ + s * 2 * L::kTile + sh * kStep * 64;
-                const uint64_t dk = smem_desc_kmajor(sb, 64), dv = smem_desc_kmajor(sb + L::kOffV, 64);
+                const uint64_t dk = smem_desc_kmajor(kt, 64), dv = smem_desc_kmajor(kt + L::kTile, 64);
                 const uint64_t dq = smem_desc_kmajor(q, 64), dd = smem_desc_kmajor(q + L::kTile, 64);
                 const uint32_t col = tm + (u & 1) * 128;
                 if (elect_one()) {
@@ -479,27 +557,30 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                             umma_i8(col + kStep, dv + o, dd + o, kIdS, x ? 1u : 0u);
                         }
                     }
+                    if (u + 1 == w.nu) umma_commit(bar_ke + 8 * (kn % L::KS));
                     umma_commit(bar_sf + 8 * (u & 1));
                 }
                 __syncwarp();
-                if (++sk == per) sk = 0, sh = 0, ++sw;
+                if (++sk == w.per) sk = 0, sh = 0, ++sw;
                 else if ((sh ^= 1) == 0) ++sw;
                 return true;
             };
-            if (ok) ok = scores(0);
-            for (int u = 0; u < nu && ok; ++u) {
-                if (u + 1 < nu) {
-                    if (u > 0) ok = wait(bar_ee, (u - 1) & 1);
+            if (pn > 0 && !(ok = wait(bar_ee, pn - 1))) break;
+            ok = scores(0);
+            for (int u = 0; u < w.nu && ok; ++u) {
+                if (u + 1 < w.nu) {
+                    if (u > 0) ok = wait(bar_ee, pn - 1);
                     if (!ok || !(ok = scores(u + 1))) break;
                 }
-                if (!(ok = wait(bar_ef + 8 * (u & 1), (u >> 1) & 1))) break;
+                if (!(ok = wait(bar_ef + 8 * (u & 1), (ef_par >> (u & 1)) & 1))) break;
+                ef_par ^= 1u << (u & 1);
+                if (u == 0 && on > 0 && !(ok = wait(bar_oe, on - 1))) break;  // the last item's gradients are read
                 tc_fence_after();
                 const int s = pw % L::QS;
                 const uint32_t q = sb + L::kOffQ + s * 2 * L::kTile + ph * kStep * 64;
                 const uint64_t dq = smem_desc_mnmajor64(q, kHalfTile), dd = smem_desc_mnmajor64(q + L::kTile, kHalfTile);
                 const uint32_t e0 = tm + (u & 1) * 128, first = u ? 1u : 0u;
-                const bool done = pk_ + 1 == per || ph == 1;
-                constexpr int kDk = MODE == 3 ? kAccCol + 2 * DP : kAccCol;
+                const bool done = pk_ + 1 == w.per || ph == 1;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
@@ -514,121 +595,194 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                     }
                     if (done) umma_commit(bar_qe + 8 * s);
                     umma_commit(bar_ee);
+                    if (u + 1 == w.nu) umma_commit(bar_of);
                 }
                 __syncwarp();
-                if (++pk_ == per) pk_ = 0, ph = 0, ++pw;
+                ++pn;
+                if (++pk_ == w.per) pk_ = 0, ph = 0, ++pw;
                 else if ((ph ^= 1) == 0) ++pw;
             }
-            if (!ok && lane == 0) fail();
-            if (elect_one()) {
-                umma_commit(bar_of);
-                umma_commit(bar_dr);
-            }
-            __syncwarp();
-            wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
+            ++kn;
+            ++on;
         }
+        if (!ok && lane == 0) fail();
+        if (elect_one()) umma_commit(bar_dr);
+        __syncwarp();
+        wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
     } else if (warp == kSoftWarps + 2) {
-        // ------------------------------------------------------------ the queries' vectors
-        // two queries per lane and step, read one step ahead
-        int2 st[2], rw[2];
-        auto fetch = [&](int u) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int i = base + (u % per) * kStep + 2 * lane + k;
-                st[k] = rw[k] = make_int2(0, 0);
-                if (u < nu && i < nq) {
-                    const int64_t at = ((int64_t)b * a.Hq + g * a.rep + u / per) * a.Lq + i;
-                    st[k] = a.stats[at];
-                    if (MODE & 2) rw[k] = a.row[at];
-                }
-            }
-        };
+        // ------------------------------------------------------------ the items' exponents and the queries' vectors
         bool ok = true;
-        if (nu > 0) fetch(0);
-        for (int u = 0; u < nu && ok; ++u) {
-            float m[2], r[2], d[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                // a query that sees nothing, or none: every score lies below its maximum, and r = 0
-                m[k] = -(kAttnMagic + (st[k].y > 0 ? (float)st[k].x : 4194304.0f));
-                r[k] = attn_rho(st[k].y, pi);
-                d[k] = -(kAttnMagic + (float)rw[k].x);
+        int xn = 0, ln = 0, cn = 0;  // items of few, of many queries; steps
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+            const KeyItem w = key_item(a, item);
+            const int64_t row0 = ((int64_t)w.b * a.Hq + w.g * a.rep) * a.Lq;
+            int pi = 0, c = 0;
+            if (is_long(w)) {
+                long_exponents(w, ln & 1, -1, pi, c);  // (the softmax warps meet here after a failure too)
+                ++ln;
+                if (!ok) continue;
+            } else {
+                if (!ok) continue;
+                const int total = w.n * a.rep;
+                int m = INT_MAX;
+#pragma unroll 4
+                for (int t = lane; t < total; t += 32) {
+                    const int S = a.stats[row_of(w, t)].y;
+                    m = S > 0 ? min(m, S) : m;
+                }
+                m = -warp_max(-m);
+                pi = m == INT_MAX ? 0 : 31 - __clz(m);
+                if (MODE & 2) {
+                    unsigned long long x = 0;
+#pragma unroll 4
+                    for (int t = lane; t < total; t += 32) {
+                        const int64_t at = row_of(w, t);
+                        const int S = a.stats[at].y;
+                        if (S > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), a.tmax[at], a.row[at].y));
+                    }
+                    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    c = max(0, 64 - __clzll((long long)x) - 14);
+                }
+                const int xs = xn & 1;
+                if (xn >= 2) ok = __all_sync(0xffffffffu, wait_bar(bar_xe + 8 * xs, ((xn >> 1) - 1) & 1, lim.wait_ns, abort_flag));
+                if (!ok) {
+                    if (lane == 0) fail();
+                    continue;
+                }
+                if (lane == 0) {
+                    misc[4 + 2 * xs] = pi;
+                    misc[5 + 2 * xs] = c;
+                    mbar_arrive(bar_xf + 8 * xs);
+                }
+                ++xn;
             }
-            fetch(u + 1);
-            const int s = u & 3;
-            if (u >= 4) ok = __all_sync(0xffffffffu, wait_bar(bar_ce + 8 * s, ((u >> 2) - 1) & 1, lim.wait_ns, abort_flag));
-            float *v = (float *)(smem + L::kOffVec) + s * 3 * kStep + 2 * lane;
-            *reinterpret_cast<float2 *>(v) = make_float2(m[0], m[1]);
-            *reinterpret_cast<float2 *>(v + kStep) = make_float2(r[0], r[1]);
-            *reinterpret_cast<float2 *>(v + 2 * kStep) = make_float2(d[0], d[1]);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar_cf + 8 * s);
+            // two queries per lane and step, read one step ahead
+            int2 st[2], rw[2];
+            auto fetch = [&](int u) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int i = w.base + (u % w.per) * kStep + 2 * lane + k;
+                    st[k] = rw[k] = make_int2(0, 0);
+                    if (u < w.nu && i < w.nq) {
+                        const int64_t at = row0 + (int64_t)(u / w.per) * a.Lq + i;
+                        st[k] = a.stats[at];
+                        if (MODE & 2) rw[k] = a.row[at];
+                    }
+                }
+            };
+            if (w.nu > 0) fetch(0);
+            for (int u = 0; u < w.nu && ok; ++u) {
+                float mm[2], r[2], d[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    // a query that sees nothing, or none: every score lies below its maximum, and r = 0
+                    mm[k] = -(kAttnMagic + (st[k].y > 0 ? (float)st[k].x : 4194304.0f));
+                    r[k] = attn_rho(st[k].y, pi);
+                    d[k] = -(kAttnMagic + (float)rw[k].x);
+                }
+                fetch(u + 1);
+                const int s = cn & 3;
+                if (cn >= 4) ok = __all_sync(0xffffffffu, wait_bar(bar_ce + 8 * s, ((cn >> 2) - 1) & 1, lim.wait_ns, abort_flag));
+                float *v = (float *)(smem + L::kOffVec) + s * 3 * kStep + 2 * lane;
+                *reinterpret_cast<float2 *>(v) = make_float2(mm[0], mm[1]);
+                *reinterpret_cast<float2 *>(v + kStep) = make_float2(r[0], r[1]);
+                *reinterpret_cast<float2 *>(v + 2 * kStep) = make_float2(d[0], d[1]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_cf + 8 * s);
+                ++cn;
+            }
         }
         if (!ok && lane == 0) fail();
     } else {
         // ------------------------------------------------------------ softmax: lane = key
-        const int wg = warp >> 2, et = threadIdx.x & 127, j = j0 + et, pair = wg >> 1, c0 = (wg & 1) * 32;
+        named_bar_sync(3, NS + 32);
+        tc_fence_after();
+        const uint32_t tm = (uint32_t)misc[0];
+        const int wg = warp >> 2, et = threadIdx.x & 127, pair = wg >> 1, c0 = (wg & 1) * 32;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const f2 f = pk(attn_factor(a, bg)), sc = pk(pow2f(-cexp));
-        const int lo_i = a.causal ? j - off : 0;  // the first query that sees this key
-        const int lo_max = warp_max(lo_i);
         bool ok = true;
-        int k_in = pair % max(per, 1);
-        for (int u = pair; u < nu && ok; u += 2) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, (u >> 1) & 1, lim.wait_ns, abort_flag) &&
-                                             wait_bar(bar_cf + 8 * (u & 3), (u >> 2) & 1, lim.wait_ns, abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            const float *vec = (const float *)(smem + L::kOffVec) + (u & 3) * 3 * kStep + c0;
-            const int i = base + k_in * kStep + c0;
-            const uint32_t mine = tm + lanes + pair * 128 + c0;
-#pragma unroll 1
-            for (int c = 0; c < 32; c += 16) {
-                uint32_t vs[16], vd[16], plo[4], phi[4], ulo[4], uhi[4];
-                tmem_ld16(mine + c, vs);
-                if (MODE & 2) tmem_ld16(mine + kStep + c, vd);
-                tmem_ld_wait();
-                tmem_tie(vs);
-                if (MODE & 2) tmem_tie(vd);
-                if (i + c >= lo_max) dkv16<false, MODE>(vs, vd, vec + c, f, sc, 0, plo, phi, ulo, uhi);
-                else dkv16<true, MODE>(vs, vd, vec + c, f, sc, lo_i - i - c, plo, phi, ulo, uhi);
-                if (MODE & 1) {  // in the place of scores already read
-                    tmem_st4(mine + c / 4, phi);
-                    tmem_st4(mine + 8 + c / 4, plo);
-                }
-                if (MODE & 2) {
-                    tmem_st4(mine + kStep + c / 4, uhi);
-                    tmem_st4(mine + kStep + 8 + c / 4, ulo);
-                }
+        int on = 0, sn = 0, xn = 0, ln = 0, cn = 0;  // outputs, this pair's steps, items of few and of many queries, all steps
+        for (int item = blockIdx.x; item < items; item += gridDim.x) {  // (outputs are written after a failure too)
+            const KeyItem w = key_item(a, item);
+            const int j = w.j0 + et;
+            int pi, cexp;
+            if (is_long(w)) {
+                long_exponents(w, ln & 1, (int)threadIdx.x, pi, cexp);
+                ++ln;
+            } else {
+                const int xs = xn & 1;
+                ok = ok && __all_sync(0xffffffffu, wait_bar(bar_xf + 8 * xs, (xn >> 1) & 1, lim.wait_ns, abort_flag));
+                pi = misc[4 + 2 * xs], cexp = misc[5 + 2 * xs];
+                warp_arrive(bar_xe + 8 * xs);
+                ++xn;
             }
-            tmem_st_wait();
-            warp_arrive(bar_ef + 8 * pair);
-            if (lane == 0) mbar_arrive(bar_ce + 8 * (u & 3));
-            if ((k_in += 2) >= per) k_in %= per;
-        }
-        if (nu > 0 && ok) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar_of, 0, lim.wait_ns, abort_flag));
-            tc_fence_after();
+            const f2 f = pk(attn_factor(a, w.bg)), sc = pk(pow2f(-cexp));
+            const int lo_i = a.causal ? j - w.off : 0;  // the first query that sees this key
+            const int lo_max = warp_max(lo_i);
+            int k_in = w.per > 0 ? pair % w.per : 0;
+            for (int u = pair; u < w.nu && ok; u += 2) {
+                const int cs = (cn + u) & 3;
+                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, sn & 1, lim.wait_ns, abort_flag) &&
+                                                 wait_bar(bar_cf + 8 * cs, ((cn + u) >> 2) & 1, lim.wait_ns, abort_flag));
+                if (!ok) break;
+                ++sn;
+                tc_fence_after();
+                const float *vec = (const float *)(smem + L::kOffVec) + cs * 3 * kStep + c0;
+                const int i = w.base + k_in * kStep + c0;
+                const uint32_t mine = tm + lanes + pair * 128 + c0;
+#pragma unroll 1
+                for (int c = 0; c < 32; c += 16) {
+                    uint32_t vs[16], vd[16], plo[4], phi[4], ulo[4], uhi[4];
+                    tmem_ld16(mine + c, vs);
+                    if (MODE & 2) tmem_ld16(mine + kStep + c, vd);
+                    tmem_ld_wait();
+                    tmem_tie(vs);
+                    if (MODE & 2) tmem_tie(vd);
+                    if (i + c >= lo_max) dkv16<false, MODE>(vs, vd, vec + c, f, sc, 0, plo, phi, ulo, uhi);
+                    else dkv16<true, MODE>(vs, vd, vec + c, f, sc, lo_i - i - c, plo, phi, ulo, uhi);
+                    if (MODE & 1) {  // in the place of scores already read
+                        tmem_st4(mine + c / 4, phi);
+                        tmem_st4(mine + 8 + c / 4, plo);
+                    }
+                    if (MODE & 2) {
+                        tmem_st4(mine + kStep + c / 4, uhi);
+                        tmem_st4(mine + kStep + 8 + c / 4, ulo);
+                    }
+                }
+                tmem_st_wait();
+                warp_arrive(bar_ef + 8 * pair);
+                if (lane == 0) mbar_arrive(bar_ce + 8 * cs);
+                if ((k_in += 2) >= w.per) k_in %= w.per;
+            }
+            cn += w.nu;
+            if (w.nu > 0 && ok) {
+                ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
+                tc_fence_after();
+            }
+            const bool live = j < a.Lk, read = w.nu > 0 && ok;
+            const int ed = attn_top(a, OPD, w.bg), ev = attn_top(a, OPV, w.bg), eq = attn_top(a, OPQ, w.bg);
+            // 32 columns of one gradient per warpgroup
+            const bool is_k = MODE == 3 ? wg >= 2 : MODE == 2;
+            const int cc = MODE == 3 ? (wg & 1) * 32 : wg * 32, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
+            float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 8 * 128 : 0) + et;
+            const int den = read && j < w.nk ? 1 : 0;
+            const bool narrow = (int64_t)w.nq * a.rep <= 1024;
+            const int bar = MODE == 3 ? 1 + (wg >> 1) : 1, nthr = MODE == 3 ? NS / 2 : NS;
+            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, (int64_t)w.b * a.Lk + j, w.g, cc, den, is_k ? a.mul : 1,
+                            is_k ? cexp - pi - a.shift + ed + ev + eq : ed - pi, live, narrow, gm, 128, bar, nthr,
+                            AccCols{tm + lanes + acc, DP, read});
+            if (w.nu > 0) {
+                warp_arrive(bar_oe);
+                ++on;
+            }
+            named_bar_sync(bar, nthr);  // the shared maxima are read before the next item's are written
         }
         if (!ok && lane == 0) fail();
-        const bool live = j < a.Lk, read = nu > 0 && ok;
-        const int ed = attn_top(a, OPD, bg), ev = attn_top(a, OPV, bg), eq = attn_top(a, OPQ, bg);
-        // 32 columns of one gradient per warpgroup
-        const bool is_k = MODE == 3 ? wg >= 2 : MODE == 2;
-        const int cc = MODE == 3 ? (wg & 1) * 32 : wg * 32, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
-        float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 8 * 128 : 0) + et;
-        const int64_t row = (int64_t)b * a.Lk + j;
-        const int den = read && j < nk ? 1 : 0;
-        const bool narrow = (int64_t)nq * a.rep <= 1024;
-        const int bar = MODE == 3 ? 1 + (wg >> 1) : 1, nthr = MODE == 3 ? 256 : 32 * kSoftWarps;
-        const AttnOut &out = is_k ? a.dk : a.dv;
-        const int mul = is_k ? a.mul : 1, r = is_k ? cexp - pi - a.shift + ed + ev + eq : ed - pi;
-        fit_row_tmem<2>(a, out, row, g, cc, den, mul, r, live, narrow, gm, 128, bar, nthr, AccCols{tm + lanes + acc, DP, read});
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == kSoftWarps + 1) tmem_dealloc(tm, 512);
+    if (warp == kSoftWarps + 1) tmem_dealloc(__shfl_sync(0xffffffffu, (uint32_t)misc[0], 0), 512);
 }
 
 }  // namespace ict
