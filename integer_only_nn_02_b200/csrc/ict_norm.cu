@@ -92,7 +92,7 @@ struct NormArgs {
     int N, nvec;                    // columns, 16-column vectors of a row
     int gvx, gvd, gvg, gvb, gvo;    // vectors per group
     int ngx, ngd, ngg, ngb, ngo;    // groups per row
-    int fast;                       // an output group is a power of two of neighbouring lanes
+    int fast, gso;                  // an output group is a power of two of neighbouring lanes, its log2
     int eps_mul, eps_shift;
     float4 *stat;                   // backward: {S1, R, row exponent, 0} of every row
     int32_t *col_top;               // backward: largest exponent of dY's column groups
@@ -171,14 +171,15 @@ __device__ __forceinline__ uint4 fit16(const f2 (&y)[8], uint32_t top, int base,
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 __device__ __forceinline__ uint32_t max16(const f2 (&y)[8]) {
-    float m = 0;
+    float m0 = 0, m1 = 0;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         float a, b;
         unpk(y[q], a, b);
-        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+        m0 = fmaxf(m0, fabsf(a));
+        m1 = fmaxf(m1, fabsf(b));
     }
-    return __float_as_uint(m);
+    return __float_as_uint(fmaxf(m0, m1));
 }
 
 // Tables of per-column floats in shared memory: 4 floats of vector q's chunk k at
@@ -222,12 +223,14 @@ __device__ __forceinline__ void fit_row(const NormArgs &p, int64_t row, bool liv
             eval(v, y);
             uint32_t m = max16(y);
             if (q >= p.nvec) m = 0;
-            for (int o = 1; o < p.gvo; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1)
+                if (o < p.gvo) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             int e;
             const uint4 w = fit16(y, m, base, e);
             if (live && q < p.nvec) {
                 *reinterpret_cast<uint4 *>(out + q * 16) = w;
-                if ((q & (p.gvo - 1)) == 0) oe[q / p.gvo] = (int8_t)e;
+                if ((q & (p.gvo - 1)) == 0) oe[q >> p.gso] = (int8_t)e;
             }
         }
         return;
@@ -262,7 +265,7 @@ __device__ __forceinline__ void fit_row(const NormArgs &p, int64_t row, bool liv
 // Bound by memory (2 bytes a value); the row stays packed in registers between the sums
 // and the output, gamma and beta stay in shared memory as floats.
 template <int L, int V>
-__global__ void __launch_bounds__(256) norm_fwd_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(256, V <= 4 ? 3 : (V <= 8 ? 2 : 1)) norm_fwd_kernel(const __grid_constant__ NormArgs p) {
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ int top;
     __shared__ RneK rk[9];
@@ -335,7 +338,7 @@ __global__ void __launch_bounds__(256) norm_fwd_kernel(const __grid_constant__ N
 // Backward with respect to the row: dX, each row's statistics for the parameter gradients,
 // and the largest exponent of every column group of dY.
 template <int L, int V>
-__global__ void __launch_bounds__(256) norm_bwd_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormArgs p) {
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ int top;
     __shared__ int cm[kMaxCols / 16];  // the block's largest exponent of every column group of dY
@@ -467,86 +470,95 @@ __global__ void __launch_bounds__(256) norm_bwd_kernel(const __grid_constant__ N
 struct NormColArgs {
     const int8_t *x, *x_exp, *dy, *dy_exp;
     int64_t rows, ldx, lddy, rows_per_block;
-    int N, gvx, gvd, ngx, ngd;
+    int N, nvec, vb, gvx, gvd, ngx, ngd;  // vb: vectors (16 columns) of a block
     const float4 *stat;
     const int32_t *col_top;
     int64_t *acc;  // [2][N]: sums of A_col(dy) h and of A_col(dy)
 };
 
-// Parameter gradients: a thread owns four columns and walks down the rows four at a time;
-// the four rows' bytes are transposed so that one dp4a adds four rows of a column.  The
-// sums are whole numbers, so their order does not matter; blocks meet by 64-bit atomics.
-__global__ void __launch_bounds__(256) norm_cols_kernel(const __grid_constant__ NormColArgs p) {
-    __shared__ int red[8][32][12];
-    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-    const int word = blockIdx.x * 32 + lane, words = p.N / 4;
-    const bool on = word < words;
-    const int wc = on ? word : words - 1;
-    const int q = wc >> 2, gx = q / p.gvx, gd = q / p.gvd;
-    const int et = p.col_top[gd];
-    const f2 N2 = pk((float)p.N), mg = pk(kMagic);
-    int lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0}, sb[4] = {0, 0, 0, 0};
-    const int64_t r1 = min(p.rows, (int64_t)(blockIdx.y + 1) * p.rows_per_block);
-    for (int64_t r = (int64_t)blockIdx.y * p.rows_per_block + wp * 4; r < r1; r += 32) {
-        uint32_t dw[4];
-        uint32_t hb[4][2];  // per row: columns 0 1 and 2 3 as [lo, lo, hi, hi] bytes
+// Parameter gradients: a thread owns 16 columns and walks down the rows four at a time; the four
+// rows' bytes of a column are brought into one word, so that a dp4a adds four rows.  h goes in as
+// its low and high byte.  The sums are whole numbers, so their order does not matter; threads
+// meet in shared memory and blocks by 64-bit atomics.  Wide columns per thread because of the
+// rows' addresses, exponents and statistics: with four columns they were two thirds of 28
+// instructions a value.
+__global__ void __launch_bounds__(256, 2) norm_cols_kernel(const __grid_constant__ NormColArgs p) {
+    extern __shared__ int sums[];  // [3][vb * 16]
+    __shared__ RneK rk[9];
+    const int slots = 256 / p.vb, slot = threadIdx.x / p.vb, cols = p.vb * 16;
+    const int q = blockIdx.x * p.vb + threadIdx.x % p.vb;
+    for (int t = threadIdx.x; t < 3 * cols; t += 256) sums[t] = 0;
+    rne_table_init(rk);
+    __syncthreads();
+    if (slot < slots && q < p.nvec) {
+        const int gx = q / p.gvx, gd = q / p.gvd, et = p.col_top[gd];
+        const f2 N2 = pk((float)p.N), mg = pk(kMagic);
+        int lo[16], hi[16], sb[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t row = min(r + i, p.rows - 1);
-            const float4 st = p.stat[row];
-            const uint32_t xw = *reinterpret_cast<const uint32_t *>(p.x + row * p.ldx + wc * 4);
-            uint32_t yw = *reinterpret_cast<const uint32_t *>(p.dy + row * p.lddy + wc * 4);
-            const int exx = p.x_exp[row * p.ngx + gx], edy = p.dy_exp[row * p.ngd + gd];
-            if (r + i >= r1) yw = 0;
-            // dy to the column group's exponent
-            const RneK k = rne_consts(rne_index(et, edy));
-            const uint32_t src = yw ^ 0x80808080u;
-            dw[i] = __byte_perm(fma_f16x2(__byte_perm(src, 0x64646464u, 0x4140), k.sc, k.k),
-                                fma_f16x2(__byte_perm(src, 0x64646464u, 0x4342), k.sc, k.k), 0x6420);
-            // a = RNE(C 2^(e - e_row)), then h as in the row kernels
-            const int es = __float_as_int(st.z);
-            const f2 sc = pk(exx == kEZero ? 0.0f : pow2f(exx - es));
-            const f2 ms = pk(-st.x), R2 = pk(st.y * 256.0f), nmg = pk(-kMagic);
-            const uint32_t xb = xw ^ 0x80808080u;
-            float h0, h1, h2, h3;
-            const f2 a0 = add2(fma2(bytes2(xb, 0), sc, mg), nmg), a1 = add2(fma2(bytes2(xb, 2), sc, mg), nmg);
-            unpk(fma2(fma2(N2, a0, ms), R2, mg), h0, h1);
-            unpk(fma2(fma2(N2, a1, ms), R2, mg), h2, h3);
-            hb[i][0] = __byte_perm(__float_as_uint(h0), __float_as_uint(h1), 0x5140);
-            hb[i][1] = __byte_perm(__float_as_uint(h2), __float_as_uint(h3), 0x5140);
+        for (int c = 0; c < 16; ++c) lo[c] = hi[c] = sb[c] = 0;
+        const int64_t r1 = min(p.rows, (int64_t)(blockIdx.y + 1) * p.rows_per_block);
+        for (int64_t r = (int64_t)blockIdx.y * p.rows_per_block + slot * 4; r < r1; r += slots * 4) {
+            uint4 xw[4], dw[4];
+            int ex[4], ed[4];
+            float4 st[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = min(r + i, r1 - 1);
+                st[i] = p.stat[row];
+                xw[i] = *reinterpret_cast<const uint4 *>(p.x + row * p.ldx + q * 16);
+                dw[i] = *reinterpret_cast<const uint4 *>(p.dy + row * p.lddy + q * 16);
+                ex[i] = p.x_exp[row * p.ngx + gx];
+                ed[i] = r + i < r1 ? (int)p.dy_exp[row * p.ngd + gd] : kEZero;
+            }
+            f2 ms[4], R2[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dw[i] = rne_shift16_k(dw[i], rk[rne_index(et, ed[i])]);  // to the column group's exponent (0 beyond the rows)
+                xw[i] = rne_shift16_k(xw[i], rk[rne_index(__float_as_int(st[i].z), ex[i])]);  // to the row's
+                ms[i] = pk(-st[i].x);
+                R2[i] = pk(st[i].y * 256.0f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // four columns
+                const uint32_t xk[4] = {(&xw[0].x)[k] ^ 0x80808080u, (&xw[1].x)[k] ^ 0x80808080u, (&xw[2].x)[k] ^ 0x80808080u,
+                                        (&xw[3].x)[k] ^ 0x80808080u};
+                const uint32_t dk[4] = {(&dw[0].x)[k], (&dw[1].x)[k], (&dw[2].x)[k], (&dw[3].x)[k]};
+                // rows 0..3 of column c as the bytes of one word
+                const uint32_t d01a = __byte_perm(dk[0], dk[1], 0x5140), d23a = __byte_perm(dk[2], dk[3], 0x5140);
+                const uint32_t d01b = __byte_perm(dk[0], dk[1], 0x7362), d23b = __byte_perm(dk[2], dk[3], 0x7362);
+                const uint32_t dc[4] = {__byte_perm(d01a, d23a, 0x5410), __byte_perm(d01a, d23a, 0x7632),
+                                        __byte_perm(d01b, d23b, 0x5410), __byte_perm(d01b, d23b, 0x7632)};
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    float h[4][2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) unpk(fma2(fma2(N2, bytes2(xk[i], c), ms[i]), R2[i], mg), h[i][0], h[i][1]);
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const uint32_t a = __byte_perm(__float_as_uint(h[0][z]), __float_as_uint(h[1][z]), 0x5140);
+                        const uint32_t b = __byte_perm(__float_as_uint(h[2][z]), __float_as_uint(h[3][z]), 0x5140);
+                        const int at = 4 * k + c + z;
+                        lo[at] = dp4a_us(__byte_perm(a, b, 0x5410), (int)dc[c + z], lo[at]);
+                        hi[at] = __dp4a((int)__byte_perm(a, b, 0x7632), (int)dc[c + z], hi[at]);
+                        sb[at] = __dp4a(0x01010101, (int)dc[c + z], sb[at]);
+                    }
+                }
+            }
         }
-        // rows 0..3 of column c as the bytes of one word
-        const uint32_t d01a = __byte_perm(dw[0], dw[1], 0x5140), d23a = __byte_perm(dw[2], dw[3], 0x5140);
-        const uint32_t d01b = __byte_perm(dw[0], dw[1], 0x7362), d23b = __byte_perm(dw[2], dw[3], 0x7362);
-        const uint32_t dc[4] = {__byte_perm(d01a, d23a, 0x5410), __byte_perm(d01a, d23a, 0x7632),
-                                __byte_perm(d01b, d23b, 0x5410), __byte_perm(d01b, d23b, 0x7632)};
+        const int at = (threadIdx.x % p.vb) * 16;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const int b = c & 1;  // hb[i][c >> 1] = [lo0, lo1, hi0, hi1]
-            const uint32_t sl = b ? 0x5511u : 0x4400u, sh = b ? 0x7733u : 0x6622u;
-            const uint32_t l01 = __byte_perm(hb[0][c >> 1], hb[1][c >> 1], sl), l23 = __byte_perm(hb[2][c >> 1], hb[3][c >> 1], sl);
-            const uint32_t h01 = __byte_perm(hb[0][c >> 1], hb[1][c >> 1], sh), h23 = __byte_perm(hb[2][c >> 1], hb[3][c >> 1], sh);
-            // [r0, r0, r1, r1] -> bytes 0 and 2
-            const uint32_t l = __byte_perm(l01, l23, 0x6420), h = __byte_perm(h01, h23, 0x6420);
-            lo[c] = dp4a_us(l, (int)dc[c], lo[c]);
-            hi[c] = __dp4a((int)h, (int)dc[c], hi[c]);
-            sb[c] = __dp4a(0x01010101, (int)dc[c], sb[c]);
+        for (int c = 0; c < 16; ++c) {
+            atomicAdd(&sums[at + c], lo[c]);
+            atomicAdd(&sums[cols + at + c], hi[c]);
+            atomicAdd(&sums[2 * cols + at + c], sb[c]);
         }
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) red[wp][lane][c] = lo[c], red[wp][lane][4 + c] = hi[c], red[wp][lane][8 + c] = sb[c];
     __syncthreads();
-    for (int t = threadIdx.x; t < 128; t += 256) {
-        const int wl = t >> 2, c = t & 3;
-        const int64_t col = ((int64_t)blockIdx.x * 32 + wl) * 4 + c;
-        if (col >= p.N) continue;
-        int64_t a = 0, b = 0;
-        for (int w = 0; w < 8; ++w) {
-            a += (int64_t)red[w][wl][4 + c] * 256 + red[w][wl][c];
-            b += red[w][wl][8 + c];
-        }
-        atomicAdd(reinterpret_cast<unsigned long long *>(p.acc) + col, (unsigned long long)a);
-        atomicAdd(reinterpret_cast<unsigned long long *>(p.acc) + p.N + col, (unsigned long long)b);
+    for (int t = threadIdx.x; t < cols; t += 256) {
+        const int64_t col = (int64_t)blockIdx.x * cols + t;
+        if (col >= p.N) break;
+        atomicAdd(reinterpret_cast<unsigned long long *>(p.acc) + col, (unsigned long long)((int64_t)sums[cols + t] * 256 + sums[t]));
+        atomicAdd(reinterpret_cast<unsigned long long *>(p.acc) + p.N + col, (unsigned long long)(int64_t)sums[2 * cols + t]);
     }
 }
 
@@ -707,6 +719,7 @@ void dispatch(int nvec, F &&f) {
 template <int L>
 void finish_plan(NormArgs &a) {
     a.fast = (a.gvo & (a.gvo - 1)) == 0 && a.gvo <= L && a.nvec % a.gvo == 0;
+    a.gso = a.fast ? __builtin_ctz((unsigned)a.gvo) : 0;
 }
 
 template <typename K>
@@ -807,11 +820,13 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
         c.x = a.x, c.x_exp = a.x_exp, c.dy = a.dy, c.dy_exp = a.dy_exp, c.rows = a.rows, c.ldx = a.ldx, c.lddy = a.lddy;
         c.N = a.N, c.gvx = a.gvx, c.gvd = a.gvd, c.ngx = a.ngx, c.ngd = a.ngd;
         c.stat = a.stat, c.col_top = a.col_top, c.acc = acc;
-        // four blocks per SM, at least 32 rows and at most 2^15 rows each (the 32-bit sums)
-        const int64_t tiles = host::cdiv(a.N, 128);
-        const int64_t want = std::max<int64_t>(1, (int64_t)sms * 4 / tiles);
-        c.rows_per_block = std::min<int64_t>(1 << 15, host::round_up(std::max<int64_t>(1, host::cdiv(a.rows, want)), 32));
-        norm_cols_kernel<<<dim3((unsigned)tiles, (unsigned)host::cdiv(a.rows, c.rows_per_block)), 256, 0, s>>>(c);
+        // two blocks per SM, at least 64 rows and at most 2^15 rows each (the 32-bit sums)
+        c.nvec = a.nvec;
+        c.vb = a.nvec <= 64 ? a.nvec : 32;
+        const int64_t tiles = host::cdiv(a.nvec, c.vb);
+        const int64_t want = std::max<int64_t>(1, (int64_t)sms * 2 / tiles);
+        c.rows_per_block = std::min<int64_t>(1 << 15, host::round_up(std::max<int64_t>(1, host::cdiv(a.rows, want)), 64));
+        norm_cols_kernel<<<dim3((unsigned)tiles, (unsigned)host::cdiv(a.rows, c.rows_per_block)), 256, (size_t)c.vb * 16 * 12, s>>>(c);
         host::counted(1);
     }
     NormFitArgs f;
