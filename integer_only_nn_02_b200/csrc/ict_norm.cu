@@ -95,7 +95,7 @@ struct NormArgs {
     int fast, gso;                  // an output group is a power of two of neighbouring lanes, its log2
     int eps_mul, eps_shift;
     float4 *stat;                   // backward: {S1, R, row exponent, 0} of every row
-    int32_t *col_top;               // backward: largest exponent of dY's column groups
+    int32_t *col_top;               // backward: largest exponent of dY's column groups + 256 (0: all zero)
 };
 
 // (R, h's multiplier) of a row: D is formed exactly, then rounded to 24 bits, its root
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __g
         if (v * L + lr < p.nvec && ctop[v] > kNoExp) atomicMax(&cm[gd[v]], ctop[v]);
     __syncthreads();
     for (int g = threadIdx.x; g < p.ngd; g += blockDim.x)
-        if (cm[g] > kNoExp) atomicMax(&p.col_top[g], cm[g]);
+        if (cm[g] > kNoExp) atomicMax(&p.col_top[g], cm[g] + 256);
 }
 
 struct NormColArgs {
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(256, 2) norm_cols_kernel(const __grid_constant
     rne_table_init(rk);
     __syncthreads();
     if (slot < slots && q < p.nvec) {
-        const int gx = q / p.gvx, gd = q / p.gvd, et = p.col_top[gd];
+        const int gx = q / p.gvx, gd = q / p.gvd, et = p.col_top[gd] - 256;
         const f2 N2 = pk((float)p.N), mg = pk(kMagic);
         int lo[16], hi[16], sb[16];
 #pragma unroll
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(256) norm_fit_kernel(const __grid_constant__ N
     const int j0 = g * G, j1 = min(p.N, j0 + G);
     if (j0 >= p.N) return;
     const int64_t *acc = p.acc + (int64_t)z * p.N;
-    auto expo = [&](int j) { return p.col_top[(j >> 4) / p.gvd] - (z == 0 ? 8 : 0); };
+    auto expo = [&](int j) { return p.col_top[(j >> 4) / p.gvd] - 256 - (z == 0 ? 8 : 0); };
     int top = kNoExp;
     for (int j = j0 + lane; j < j1; j += 32) {
         const int64_t v = acc[j];
@@ -801,9 +801,7 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
     const int64_t top_bytes = host::round_up(a.N / 4 + 4, 256);
     a.col_top = (int32_t *)((uint8_t *)ws + acc_bytes);
     a.stat = (float4 *)((uint8_t *)ws + acc_bytes + top_bytes);
-    if (cudaMemsetAsync(acc, 0, (size_t)acc_bytes, s) != cudaSuccess ||
-        cudaMemsetAsync(a.col_top, 0x80, (size_t)top_bytes, s) != cudaSuccess)
-        return ICT_ERR_CUDA;
+    if (cudaMemsetAsync(acc, 0, (size_t)(acc_bytes + top_bytes), s) != cudaSuccess) return ICT_ERR_CUDA;
     host::Timer kt(s, ICT_KC_POINTWISE, 3.0 * (double)a.rows * a.N + (double)a.rows * (a.ngx + a.ngd + a.ngo));
     if (a.rows > 0) {
         dispatch(a.nvec, [&](auto lanes, auto vecs) {
@@ -820,12 +818,12 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
         c.x = a.x, c.x_exp = a.x_exp, c.dy = a.dy, c.dy_exp = a.dy_exp, c.rows = a.rows, c.ldx = a.ldx, c.lddy = a.lddy;
         c.N = a.N, c.gvx = a.gvx, c.gvd = a.gvd, c.ngx = a.ngx, c.ngd = a.ngd;
         c.stat = a.stat, c.col_top = a.col_top, c.acc = acc;
-        // two blocks per SM, at least 64 rows and at most 2^15 rows each (the 32-bit sums)
+        // two blocks per SM, at least eight rows per thread and at most 2^15 rows each (the 32-bit sums)
         c.nvec = a.nvec;
         c.vb = a.nvec <= 64 ? a.nvec : 32;
         const int64_t tiles = host::cdiv(a.nvec, c.vb);
         const int64_t want = std::max<int64_t>(1, (int64_t)sms * 2 / tiles);
-        c.rows_per_block = std::min<int64_t>(1 << 15, host::round_up(std::max<int64_t>(1, host::cdiv(a.rows, want)), 64));
+        c.rows_per_block = std::min<int64_t>(1 << 15, host::round_up(std::max<int64_t>(1, host::cdiv(a.rows, want)), 8 * (256 / c.vb)));
         norm_cols_kernel<<<dim3((unsigned)tiles, (unsigned)host::cdiv(a.rows, c.rows_per_block)), 256, (size_t)c.vb * 16 * 12, s>>>(c);
         host::counted(1);
     }

@@ -143,7 +143,7 @@ def _stream(stream=None):
     if stream is not None:
         return ctypes.c_void_p(stream.cuda_stream)
     # the handle alone: building a torch.cuda.Stream for it takes microseconds of every call
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
 
 
 def _ptr(t: torch.Tensor | None):
@@ -417,38 +417,42 @@ def ict_softmax_ce(Z: DevCE, target: torch.Tensor, loss: torch.Tensor, dZ: DevCE
            "ict_softmax_ce")
 
 
-def _ref(t: DevCE | None):
-    if t is None:
-        return None
-    if t.mant.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.mant.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return ctypes.byref(t.c())
+def _refs(*tensors: DevCE | None):
+    """The tensors as arguments of one library call, which runs on the current device."""
+    cur, refs = torch._C._cuda_getDevice(), []
+    for t in tensors:
+        if t is not None and t.mant.get_device() != cur:
+            raise ValueError(f"tensor on {t.mant.device}, but the current device is cuda:{cur}")
+        refs.append(ctypes.byref(t.c()) if t is not None else None)
+    return refs
 
 
 def ict_layernorm_fwd(X: DevCE, gamma: DevCE, beta: DevCE | None, eps, Y: DevCE, stream=None):
     """eps = (mul, shift): the variance's epsilon mul 2^-shift."""
-    _check(lib.ict_layernorm_fwd(_ref(X), _ref(gamma), _ref(beta), int(eps[0]), int(eps[1]), _ref(Y), _stream(stream)),
-           "ict_layernorm_fwd")
+    x, g, b, y = _refs(X, gamma, beta, Y)
+    _check(lib.ict_layernorm_fwd(x, g, b, eps[0], eps[1], y, _stream(stream)), "ict_layernorm_fwd")
 
 
 def ict_layernorm_bwd_workspace(X: DevCE) -> int:
-    return int(lib.ict_layernorm_bwd_workspace(_ref(X)))
+    return lib.ict_layernorm_bwd_workspace(ctypes.byref(X.c()))
 
 
 def ict_layernorm_bwd(X: DevCE, gamma: DevCE, dY: DevCE, eps, dX: DevCE, dgamma: DevCE, dbeta: DevCE | None, ws=None,
                       stream=None):
     nbytes = 0 if ws is None else ws.numel()
-    _check(lib.ict_layernorm_bwd(_ref(X), _ref(gamma), _ref(dY), int(eps[0]), int(eps[1]), _ref(dX), _ref(dgamma),
-                                 _ref(dbeta), _ptr(ws), nbytes, _stream(stream)), "ict_layernorm_bwd")
+    x, g, dy, dx, dg, db = _refs(X, gamma, dY, dX, dgamma, dbeta)
+    _check(lib.ict_layernorm_bwd(x, g, dy, eps[0], eps[1], dx, dg, db, _ptr(ws), nbytes, _stream(stream)),
+           "ict_layernorm_bwd")
 
 
-def attn_desc(d: dict) -> ict_attn_desc:
+def attn_desc(d: dict | ict_attn_desc) -> ict_attn_desc:
     """d: batch, heads_q, heads_kv, len_q, len_k, head_dim; causal (False), scale (mul, shift) of mul 2^-shift,
     and the first columns q_col, k_col, v_col of the heads in Q, K and V (0)."""
+    if isinstance(d, ict_attn_desc):
+        return d
     mul, shift = d["scale"]
-    return ict_attn_desc(*[int(d[k]) for k in ("batch", "heads_q", "heads_kv", "len_q", "len_k", "head_dim")],
-                         int(d.get("causal", False)), int(mul), int(shift),
-                         *[int(d.get(k, 0)) for k in ("q_col", "k_col", "v_col")])
+    return ict_attn_desc(d["batch"], d["heads_q"], d["heads_kv"], d["len_q"], d["len_k"], d["head_dim"],
+                         d.get("causal", False), mul, shift, d.get("q_col", 0), d.get("k_col", 0), d.get("v_col", 0))
 
 
 def _lens(t: torch.Tensor | None, batch: int):
@@ -457,36 +461,40 @@ def _lens(t: torch.Tensor | None, batch: int):
     return _ptr(t)
 
 
-def ict_attention_workspace(backward: bool, d: dict) -> int:
-    return int(lib.ict_attention_workspace(int(backward), ctypes.byref(attn_desc(d))))
+def ict_attention_workspace(backward: bool, d: dict | ict_attn_desc) -> int:
+    return lib.ict_attention_workspace(int(backward), ctypes.byref(attn_desc(d)))
 
 
-def _stats(t: torch.Tensor, d: dict):
+def _stats(t: torch.Tensor, c: ict_attn_desc):
     assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous()
-    assert t.numel() == 2 * d["batch"] * d["heads_q"] * d["len_q"]
+    assert t.numel() == 2 * c.batch * c.heads_q * c.len_q
     return _ptr(t)
 
 
-def ict_attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE, stats: torch.Tensor, ws=None,
-                      stream=None):
+def ict_attention_fwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE,
+                      stats: torch.Tensor, ws=None, stream=None):
+    """d: the description as a dict (see attn_desc) or already made."""
+    c = attn_desc(d)
     nbytes = 0 if ws is None else ws.numel()
-    _check(lib.ict_attention_fwd(ctypes.byref(attn_desc(d)), _ref(Q), _ref(K), _ref(V), _lens(lens_q, d["batch"]),
-                                 _lens(lens_k, d["batch"]), _ref(O), _stats(stats, d), _ptr(ws), nbytes,
-                                 _stream(stream)), "ict_attention_fwd")
+    q, k, v, o = _refs(Q, K, V, O)
+    _check(lib.ict_attention_fwd(ctypes.byref(c), q, k, v, _lens(lens_q, c.batch), _lens(lens_k, c.batch), o,
+                                 _stats(stats, c), _ptr(ws), nbytes, _stream(stream)), "ict_attention_fwd")
 
 
-def ict_attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE, dO: DevCE, stats: torch.Tensor,
-                      dQ: DevCE, dK: DevCE, dV: DevCE, ws=None, stream=None):
+def ict_attention_bwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE, dO: DevCE,
+                      stats: torch.Tensor, dQ: DevCE, dK: DevCE, dV: DevCE, ws=None, stream=None):
+    c = attn_desc(d)
     nbytes = 0 if ws is None else ws.numel()
-    _check(lib.ict_attention_bwd(ctypes.byref(attn_desc(d)), _ref(Q), _ref(K), _ref(V), _lens(lens_q, d["batch"]),
-                                 _lens(lens_k, d["batch"]), _ref(O), _ref(dO), _stats(stats, d), _ref(dQ), _ref(dK),
-                                 _ref(dV), _ptr(ws), nbytes, _stream(stream)), "ict_attention_bwd")
+    q, k, v, o, do, dq, dk, dv = _refs(Q, K, V, O, dO, dQ, dK, dV)
+    _check(lib.ict_attention_bwd(ctypes.byref(c), q, k, v, _lens(lens_q, c.batch), _lens(lens_k, c.batch), o, do,
+                                 _stats(stats, c), dq, dk, dv, _ptr(ws), nbytes, _stream(stream)), "ict_attention_bwd")
 
 
 def ict_values(t: DevCE, out: torch.Tensor, stream=None):
     bf16 = {torch.float32: 0, torch.bfloat16: 1}[out.dtype]
     assert out.is_cuda and tuple(out.shape) == (t.rows, t.cols) and (t.cols <= 1 or out.stride(1) == 1)
-    _check(lib.ict_values(_ref(t), bf16, _ptr(out), out.stride(0) if t.rows > 1 else max(t.cols, 1), _stream(stream)),
+    (r,) = _refs(t)
+    _check(lib.ict_values(r, bf16, _ptr(out), out.stride(0) if t.rows > 1 else max(t.cols, 1), _stream(stream)),
            "ict_values")
 
 
@@ -636,11 +644,11 @@ def layernorm_bwd(X: DevCE, gamma: DevCE, dY: DevCE, eps=(1, 20), g_cols=32, str
 
 def attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, g_cols=32, lens_q=None, lens_k=None, stream=None):
     """(O [batch * len_q, heads_q * head_dim] in (1, g_cols) groups, stats for the backward pass).  See attn_desc for d."""
-    dev = Q.mant.device
+    dev, c = Q.mant.device, attn_desc(d)
     with _on(stream):
-        O = DevCE.empty(d["batch"] * d["len_q"], d["heads_q"] * d["head_dim"], 1, g_cols, dev)
-        stats = torch.empty((d["batch"] * d["heads_q"] * d["len_q"], 2), dtype=torch.int32, device=dev)
-        ict_attention_fwd(d, Q, K, V, lens_q, lens_k, O, stats, _ws(ict_attention_workspace(False, d), dev))
+        O = DevCE.empty(c.batch * c.len_q, c.heads_q * c.head_dim, 1, g_cols, dev)
+        stats = torch.empty((c.batch * c.heads_q * c.len_q, 2), dtype=torch.int32, device=dev)
+        ict_attention_fwd(c, Q, K, V, lens_q, lens_k, O, stats, _ws(ict_attention_workspace(False, c), dev))
     return O, stats
 
 
@@ -655,10 +663,11 @@ def attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, O: DevCE, dO: DevCE, st
             made[id(t)] = DevCE.empty(t.rows, t.cols, 1, g_cols, t.mant.device)
         return made[id(t)]
 
+    c = attn_desc(d)
     with _on(stream):
         dQ, dK, dV = like(Q), like(K), like(V)
-        ict_attention_bwd(d, Q, K, V, lens_q, lens_k, O, dO, stats, dQ, dK, dV,
-                          _ws(ict_attention_workspace(True, d), Q.mant.device))
+        ict_attention_bwd(c, Q, K, V, lens_q, lens_k, O, dO, stats, dQ, dK, dV,
+                          _ws(ict_attention_workspace(True, c), Q.mant.device))
     return dQ, dK, dV
 
 
