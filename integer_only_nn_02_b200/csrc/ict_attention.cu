@@ -250,7 +250,7 @@ Scratch scratch(const AttnArgs &a, bool back) {
         s.mx = take(n * 4);
         s.sum = take(n * 4);
         s.acc = take(n * a.Dp * 8);
-        s.scores = take(n * a.Lk * 4);
+        s.scores = take(n * host::round_up(a.Lk, 4) * 4);
         s.total = at;
         return s;
     }
@@ -358,6 +358,7 @@ int launch_few(const AttnArgs &a, const Scratch &w, cudaStream_t s) {
     FewArgs p;
     p.a = a;
     p.R = a.rep * a.Lq;
+    p.ldk = host::round_up(a.Lk, 4);
     uint8_t *base = (uint8_t *)a.top - w.top;
     p.top = a.top;
     p.mx = (int32_t *)(base + w.mx);
@@ -370,7 +371,13 @@ int launch_few(const AttnArgs &a, const Scratch &w, cudaStream_t s) {
     const unsigned qs = (unsigned)host::cdiv(p.R, kFewQ);
     few_top_kernel<<<dim3((unsigned)a.B, chunks, 2), 256, 0, s>>>(p);
     few_scores_kernel<NV><<<dim3(bg, chunks, qs), 256, 0, s>>>(p);
-    few_values_kernel<NV><<<dim3(bg, chunks, qs), 128, 0, s>>>(p);
+    // as many queries per block as there are, or an even share of them
+    switch (p.R <= kFewQ ? p.R : (int)host::cdiv(p.R, qs)) {
+        case 1: few_values_kernel<NV, 1><<<dim3(bg, chunks, 1), 128, 0, s>>>(p); break;
+        case 2: few_values_kernel<NV, 2><<<dim3(bg, chunks, 1), 128, 0, s>>>(p); break;
+        case 3: few_values_kernel<NV, 3><<<dim3(bg, chunks, (unsigned)host::cdiv(p.R, 3)), 128, 0, s>>>(p); break;
+        default: few_values_kernel<NV, 4><<<dim3(bg, chunks, qs), 128, 0, s>>>(p); break;
+    }
     few_out_kernel<<<(unsigned)host::cdiv((int64_t)bg * p.R, 8), 256, 0, s>>>(p);
     host::counted(4);
     return host::launch_status();
