@@ -90,21 +90,21 @@ __global__ void __launch_bounds__(256) attn_copy_kernel(const __grid_constant__ 
 // scanned by the block that copies.  One launch and one pass instead of a memset and two
 // launches; for heads of 197 x 64 the three operands of 768 heads take 11 us against 36 us.
 template <int NV>
-__global__ void __launch_bounds__(512) attn_align_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(256) attn_align_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ int m;
     const AttnOperand &o = a.op[blockIdx.y];
     const int bg = blockIdx.x, b = bg / a.Hkv, n = clamp_len(o.lens, b, o.L), per = o.heads / a.Hkv;
     const OperandRows r{o, b, bg - b * a.Hkv, per, 0, n, a.D / 16};
     constexpr int U = 4;
     const int rows = per * o.L;
-    if (rows * NV <= U * 512) {  // the vectors wait in registers for the block's largest exponent
+    if (rows * NV <= U * 256) {  // the vectors wait in registers for the block's largest exponent
         uint4 w[U];
         int e[U], mx = kNoExp;
         if (threadIdx.x == 0) m = kNoExp;
         __syncthreads();
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = threadIdx.x + u * 512, rw = t / NV, v = t % NV, k = per == 1 ? 0 : rw / o.L, l = rw - k * o.L;
+            const int t = threadIdx.x + u * 256, rw = t / NV, v = t % NV, k = per == 1 ? 0 : rw / o.L, l = rw - k * o.L;
             w[u] = make_uint4(0, 0, 0, 0);
             e[u] = kEZero;
             if (rw < rows && l < n && v < r.nvd) {
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(512) attn_align_kernel(const __grid_constant__
         int8_t *dst = o.copy + ((int64_t)b * o.heads + r.g * per) * o.L * a.Dp;  // the group's heads lie one after the other
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int t = threadIdx.x + u * 512;
+            const int t = threadIdx.x + u * 256;
             if (t >= rows * NV) continue;
             if (e[u] != es) w[u] = rne_shift16(w[u], rne_index(es, e[u]));
             *reinterpret_cast<uint4 *>(dst + (int64_t)t * 16) = w[u];
@@ -303,7 +303,7 @@ int align_operands(const AttnArgs &a, cudaStream_t s) {
     const unsigned bg = (unsigned)(a.B * a.Hkv);
     // a few iterations per thread, or enough heads to fill the SMs
     if (vecs <= kFuseVecs || (bg >= 148 && vecs <= 4 * kFuseVecs)) {
-        attn_align_kernel<NV><<<dim3(bg, (unsigned)a.n_op), 512, 0, s>>>(a);
+        attn_align_kernel<NV><<<dim3(bg, (unsigned)a.n_op), 256, 0, s>>>(a);
         host::counted(1);
         return host::launch_status();
     }

@@ -48,9 +48,9 @@ __global__ void __launch_bounds__(256) few_top_kernel(const __grid_constant__ Fe
         const int g = threadIdx.x - slot * H, v0 = o.col / 16 + g * nvd, g0 = v0 / o.gv, g1 = (v0 + nvd - 1) / o.gv;
         const int8_t *e = o.exp + ((int64_t)b * o.L) * o.ngc;
         int t = -128;
+        for (int k = g0; k <= g1; ++k)
 #pragma unroll 8
-        for (int l = l0 + slot; l < l1; l += slots)
-            for (int k = g0; k <= g1; ++k) t = max(t, (int)e[(int64_t)l * o.ngc + k]);
+            for (int l = l0 + slot; l < l1; l += slots) t = max(t, (int)e[(int64_t)l * o.ngc + k]);
         if (t != kEZero) atomicMax(&m[g], t + 256);
     }
     __syncthreads();

@@ -91,45 +91,134 @@ struct AccCols {
     }
 };
 
+// One output group of a row: its exponent and what rounding its quotients needs.  m: the largest
+// magnitude, w: the error scale (acc_f32) as floats; first: the group's first column.
+struct GroupFit {
+    int e;
+    float sc, lim;  // 2^(r - e) mul / den; half a step less the error bound
+};
+__device__ __forceinline__ GroupFit group_fit(const AccCols &acc, int first, int G, float m, float w, bool some, float rd,
+                                              int den, int mul, int r) {
+    // the exponents that the bounds of the largest magnitude give
+    const float q0 = m * rd, dq = fmaf(w, rd, q0) * 4.76837158203125e-07f;  // 2^-21
+    const bool zero = !(some && w > 0);
+    const int n0 = zero ? 0 : need_rel_f32(__float_as_uint(fmaxf(q0 - dq, 1.17549435e-38f)), 8);
+    const int n1 = zero ? 0 : need_rel_f32(__float_as_uint(q0 + dq), 8);
+    int need = n1;
+    bool none = zero;
+    if (__any_sync(0xffffffffu, n0 != n1)) {  // exact: the largest magnitude as a whole number
+        double best = 0;
+#pragma unroll 1
+        for (int c = first; c < first + G; ++c) best = fmax(best, fabs(acc.exact(c)));
+        none = zero || best == 0;
+        if (!none) need = need_quot(best * (double)mul / (double)den);
+    }
+    GroupFit f;
+    f.e = none ? kEZero : finalize_exp(need + r);
+    f.sc = none ? 0.0f : rd * pow2f(min(max(r - f.e, -126), 100));
+    f.lim = fmaf(w * f.sc, -9.5367431640625e-07f, 0.4999999f);  // w sc 2^-20
+    return f;
+}
+
+// 16 mantissas of a group from its accumulators as floats, stored to dst (live).
+__device__ __forceinline__ void round16(const AccCols &acc, int col, const float (&n)[16], const GroupFit &f, bool some,
+                                        int den, int mul, int r, bool live, int8_t *dst) {
+    uint32_t v[16], near = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        const float w = fmaf(n[q], f.sc, kAttnMagic);
+        const float d = fmaf(n[q], f.sc, kAttnMagic - w);  // what the rounding took away
+        if (!(fabsf(d) < f.lim)) near |= 1u << q;
+        v[q] = __float_as_uint(w);
+    }
+    uint32_t w0 = pack4b(v[0], v[1], v[2], v[3]), w1 = pack4b(v[4], v[5], v[6], v[7]);
+    uint32_t w2 = pack4b(v[8], v[9], v[10], v[11]), w3 = pack4b(v[12], v[13], v[14], v[15]);
+    const bool capped = f.e == 127;
+    if (capped) near = 0xffff;
+    uint32_t todo = __reduce_or_sync(0xffffffffu, near);
+    if (todo) {
+        const double rden = f.e == kEZero || !some ? 0.0 : pow2d(r - f.e) * (double)mul / (double)den;
+        while (todo) {
+            const int q = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const double x = acc.exact(col + q);
+            if (near >> q & 1) {
+                const int y = capped ? (int)fmin(fmax(x * rden, -127.0), 127.0) : quot_mant_fast(x, rden);
+                const uint32_t sh = 8 * (q & 3), keep = ~(0xffu << sh), put = (uint32_t)(y & 0xff) << sh;
+                const int k = q >> 2;
+                w0 = k == 0 ? (w0 & keep) | put : w0;
+                w1 = k == 1 ? (w1 & keep) | put : w1;
+                w2 = k == 2 ? (w2 & keep) | put : w2;
+                w3 = k == 3 ? (w3 & keep) | put : w3;
+            }
+        }
+    }
+    if (live) *reinterpret_cast<uint4 *>(dst) = make_uint4(w0, w1, w2, w3);
+}
+
 // FIT of one row's accumulators (this thread's TMEM lane): quotients (256 hi + lo) mul / den at
-// exponent r, SEGS segments of 16 columns from column c0 of head h.  The threads that share a
-// row join their segments' maxima in gmax (shared memory, [segment][stride], two floats each).
+// exponent r, SEGS segments of 16 columns from column c0 of head h.
 // Magnitudes and mantissas are computed in fp32 with an error bound; what lies within the bound
 // of a border between two results (a mantissa in some ten thousand) is read again and decided
 // in fp64, where the quotient's rounding to 53 bits cannot hide the border.  narrow: the
-// accumulators 256 hi + lo fit 32 bits.
+// accumulators 256 hi + lo fit 32 bits.  Groups of 32 columns inside this thread's columns stay
+// in registers between the maximum and the rounding; for other groups the threads that share
+// the row join their segments' maxima in gmax (shared memory, [segment][stride]) and read the
+// accumulators twice.
 template <int SEGS>
 __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &out, int64_t row, int h, int c0, int den,
                                              int mul, int r, bool live, bool narrow, float2 *gmax, int stride, int bar,
                                              int nthreads, const AccCols &acc) {
     const int col = out.col + h * a.D;
+    const int gs = out.G / 16;  // segments of a group
+    const bool some = live && den != 0;
+    // relative error below 2^-22 (two roundings); a quotient's, accumulator included, below err 2^-21
+    const float rd = some ? __fdiv_rn((float)mul, (float)den) : 0.0f;
+    int8_t *dst = out.mant + row * out.ld + col, *oe = out.exp + row * out.ngc + col / out.G;
+    if (SEGS % 2 == 0 && gs == 2 && narrow) {
+#pragma unroll 1
+        for (int s = 0; s < SEGS; s += 2) {
+            const int c = c0 + 16 * s;
+            if (c >= a.D) break;
+            float n0[16], n1[16];
+            uint32_t hi[16], lo[16];
+            int mi = 0;
+            acc.load16(c, hi, lo);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int x = (int)hi[q] * 256 + (int)lo[q];
+                mi = max(mi, abs(x));
+                n0[q] = (float)x;
+            }
+            acc.load16(c + 16, hi, lo);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const int x = (int)hi[q] * 256 + (int)lo[q];
+                mi = max(mi, abs(x));
+                n1[q] = (float)x;
+            }
+            const GroupFit f = group_fit(acc, c, 32, (float)mi, (float)mi, some, rd, den, mul, r);
+            if (live) oe[c / 32] = (int8_t)f.e;
+            round16(acc, c, n0, f, some, den, mul, r, live, dst + c);
+            round16(acc, c + 16, n1, f, some, den, mul, r, live, dst + c + 16);
+        }
+        return;
+    }
 #pragma unroll 1
     for (int s = 0; s < SEGS; ++s) {
         uint32_t hi[16], lo[16];
         acc.load16(c0 + 16 * s, hi, lo);
         float m = 0, w = 0;
-        if (narrow) {
-            int mi = 0;
 #pragma unroll
-            for (int q = 0; q < 16; ++q) mi = max(mi, abs((int)hi[q] * 256 + (int)lo[q]));
-            m = w = (float)mi;
-        } else {
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                float e;
-                m = fmaxf(m, fabsf(acc_f32(hi[q], lo[q], false, e)));
-                w = fmaxf(w, e);
-            }
+        for (int q = 0; q < 16; ++q) {
+            float e;
+            m = fmaxf(m, fabsf(acc_f32(hi[q], lo[q], narrow, e)));
+            w = fmaxf(w, e);
         }
         gmax[(c0 / 16 + s) * stride] = make_float2(m, w);
     }
     named_bar_sync(bar, nthreads);
-    const int gs = out.G / 16;  // segments of a group
-    const bool some = live && den != 0;
-    // relative error below 2^-22 (two roundings); a quotient's, accumulator included, below err 2^-21
-    const float rd = some ? __fdiv_rn((float)mul, (float)den) : 0.0f;
-    int e = kEZero;
-    float sc = 0, lim = 0.5f;
+    GroupFit f{kEZero, 0.0f, 0.5f};
 #pragma unroll 1
     for (int s = 0; s < SEGS; ++s) {
         const int seg = c0 / 16 + s;
@@ -142,59 +231,18 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
                 m = fmaxf(m, v.x);
                 w = fmaxf(w, v.y);
             }
-            // the exponents that the bounds of the largest magnitude give
-            const float q0 = m * rd, dq = fmaf(w, rd, q0) * 4.76837158203125e-07f;  // 2^-21
-            const bool zero = !(some && w > 0);
-            const int n0 = zero ? 0 : need_rel_f32(__float_as_uint(fmaxf(q0 - dq, 1.17549435e-38f)), 8);
-            const int n1 = zero ? 0 : need_rel_f32(__float_as_uint(q0 + dq), 8);
-            int need = n1;
-            bool none = zero;
-            if (__any_sync(0xffffffffu, n0 != n1)) {  // exact: the largest magnitude as a whole number
-                double best = 0;
-#pragma unroll 1
-                for (int c = g * out.G; c < (g + 1) * out.G; ++c) best = fmax(best, fabs(acc.exact(c)));
-                none = zero || best == 0;
-                if (!none) need = need_quot(best * (double)mul / (double)den);
-            }
-            e = none ? kEZero : finalize_exp(need + r);
-            sc = none ? 0.0f : rd * pow2f(min(max(r - e, -126), 100));
-            lim = fmaf(w * sc, -9.5367431640625e-07f, 0.4999999f);  // half a step less the bound: w sc 2^-20
-            if (live && seg % gs == 0) out.exp[row * out.ngc + col / out.G + g] = (int8_t)e;
+            f = group_fit(acc, g * out.G, out.G, m, w, some, rd, den, mul, r);
+            if (live && seg % gs == 0) oe[g] = (int8_t)f.e;
         }
         uint32_t hi[16], lo[16];
+        float n[16];
         acc.load16(seg * 16, hi, lo);
-        uint32_t near = 0;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-            const float n = narrow ? (float)((int)hi[q] * 256 + (int)lo[q]) : fmaf((float)(int)hi[q], 256.0f, (float)(int)lo[q]);
-            const float w = fmaf(n, sc, kAttnMagic);
-            const float d = fmaf(n, sc, kAttnMagic - w);  // what the rounding took away
-            if (!(fabsf(d) < lim)) near |= 1u << q;
-            hi[q] = __float_as_uint(w);
+            float er;
+            n[q] = acc_f32(hi[q], lo[q], narrow, er);
         }
-        uint32_t w0 = pack4b(hi[0], hi[1], hi[2], hi[3]), w1 = pack4b(hi[4], hi[5], hi[6], hi[7]);
-        uint32_t w2 = pack4b(hi[8], hi[9], hi[10], hi[11]), w3 = pack4b(hi[12], hi[13], hi[14], hi[15]);
-        const bool capped = e == 127;
-        if (capped) near = 0xffff;
-        uint32_t todo = __reduce_or_sync(0xffffffffu, near);
-        if (todo) {
-            const double rden = e == kEZero || !some ? 0.0 : pow2d(r - e) * (double)mul / (double)den;
-            while (todo) {
-                const int q = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const double n = acc.exact(seg * 16 + q);
-                if (near >> q & 1) {
-                    const int v = capped ? (int)fmin(fmax(n * rden, -127.0), 127.0) : quot_mant_fast(n, rden);
-                    const uint32_t sh = 8 * (q & 3), keep = ~(0xffu << sh), put = (uint32_t)(v & 0xff) << sh;
-                    const int k = q >> 2;
-                    w0 = k == 0 ? (w0 & keep) | put : w0;
-                    w1 = k == 1 ? (w1 & keep) | put : w1;
-                    w2 = k == 2 ? (w2 & keep) | put : w2;
-                    w3 = k == 3 ? (w3 & keep) | put : w3;
-                }
-            }
-        }
-        if (live) *reinterpret_cast<uint4 *>(out.mant + row * out.ld + col + seg * 16) = make_uint4(w0, w1, w2, w3);
+        round16(acc, seg * 16, n, f, some, den, mul, r, live, dst + seg * 16);
     }
 }
 
