@@ -9,8 +9,8 @@
 //                    share them; scores transposed (TMEM lane = key), so that P and U are A
 //                    operands again: P = RNE(E r), U = RNE(P x 2^-c),
 //                      dV += P^T AdO, dK += U^T AQ (two planes each)
-// Steps of 64 columns, double-buffered; two pairs of softmax warpgroups take alternate steps,
-// each warpgroup 32 columns.  One block per SM (512 TMEM columns: two buffers of 64 + 64 scores
+// Steps of 64 columns in two or three buffers; two pairs of softmax warpgroups take alternate
+// steps, each warpgroup 32 columns.  One block per SM (512 TMEM columns: two buffers of 64 + 64 scores
 // and 256 columns of accumulators).  For heads wider than 64 columns dV and dK do not fit side
 // by side: one block computes dV, another dK.
 // Bound by the elementwise work: per (query, key) about 9 instructions for dQ and 11 for dK and
@@ -84,18 +84,32 @@ __device__ __forceinline__ void dkv16(const uint32_t (&vs)[16], const uint32_t (
     }
 }
 
+// The row's head columns [c0, c0 + n) of a row that nothing contributes to.
+__device__ __forceinline__ void zero_row(const AttnArgs &a, const AttnOut &out, int64_t row, int h, int c0, int n) {
+    const int col = out.col + h * a.D, end = min(a.D, c0 + n);
+    for (int c = c0; c < end; c += 16) {
+        *reinterpret_cast<uint4 *>(out.mant + row * out.ld + col + c) = make_uint4(0, 0, 0, 0);
+        if (c % out.G == 0) out.exp[row * out.ngc + (col + c) / out.G] = (int8_t)kEZero;
+    }
+}
+
 template <int DP>
 struct DqCfg {
     static constexpr int H = DP / 64, kTile = H * kHalfTile, QS = 2, KS = 3, VS = 2;
+    static constexpr int NB = DP == 64 ? 3 : 2;               // score buffers (128 columns each)
+    static constexpr int kAcc = DP == 64 ? 384 : 256;         // dQ's column
     static constexpr int kOffK = QS * 2 * kTile, kOffV = kOffK + KS * kTile;  // Q stage: Q tile, dO tile
-    static constexpr int kOffRed = kOffV + VS * kTile;  // [8][128] float2, [4][128] int
-    static constexpr int kOffBar = kOffRed + 8 * 128 * 8 + 4 * 128 * 4;
-    static constexpr int kBars = 2 * (QS + KS + VS) + 2 + 2 + 4;
+    static constexpr int kOffRed = kOffV + VS * kTile;  // [2][8][128] float2, [2][4][128] int
+    static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8 + 2 * 4 * 128 * 4;
+    static constexpr int kBars = 2 * (QS + KS + VS) + 3 * NB + 4;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 64;
 };
 
-// Persistent blocks, as the forward's.
+// Persistent blocks, as the forward's.  Two pairs of softmax warpgroups take alternate steps; the
+// pairs also take turns at the items' outputs, so that one pair starts the next item meanwhile.
+// Score buffers go round over the steps of all items (step G in buffer G % NB; the pair
+// G & 1 takes it, so that a pair never waits for a phase whose forerunner is still open).
 template <int DP>
 __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
     attn_dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -109,8 +123,8 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
     const uint32_t bar_qf = sb + L::kOffBar, bar_qe = bar_qf + 8 * L::QS;
     const uint32_t bar_kf = bar_qe + 8 * L::QS, bar_ke = bar_kf + 8 * L::KS;
     const uint32_t bar_vf = bar_ke + 8 * L::KS, bar_ve = bar_vf + 8 * L::VS;
-    const uint32_t bar_sf = bar_ve + 8 * L::VS, bar_ef = bar_sf + 16;  // scores full, T written (per buffer)
-    const uint32_t bar_ee = bar_ef + 16, bar_of = bar_ee + 8, bar_oe = bar_of + 8, bar_dr = bar_oe + 8;
+    const uint32_t bar_sf = bar_ve + 8 * L::VS, bar_ef = bar_sf + 8 * L::NB;  // scores full, T written (per buffer)
+    const uint32_t bar_ee = bar_ef + 8 * L::NB, bar_of = bar_ee + 8 * L::NB, bar_oe = bar_of + 16, bar_dr = bar_oe + 8;
     volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);
     volatile int *abort_flag = &misc[1];
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -122,10 +136,11 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
         for (int s = 0; s < L::QS; ++s) mbar_init(bar_qf + 8 * s, 1), mbar_init(bar_qe + 8 * s, 1);
         for (int s = 0; s < L::KS; ++s) mbar_init(bar_kf + 8 * s, 1), mbar_init(bar_ke + 8 * s, 1);
         for (int s = 0; s < L::VS; ++s) mbar_init(bar_vf + 8 * s, 1), mbar_init(bar_ve + 8 * s, 1);
-        for (int s = 0; s < 2; ++s) mbar_init(bar_sf + 8 * s, 1), mbar_init(bar_ef + 8 * s, kSoftWarps / 2);
-        mbar_init(bar_ee, 1);
-        mbar_init(bar_of, 1);
-        mbar_init(bar_oe, kSoftWarps);
+        for (int s = 0; s < L::NB; ++s) {
+            mbar_init(bar_sf + 8 * s, 1), mbar_init(bar_ef + 8 * s, kSoftWarps / 2), mbar_init(bar_ee + 8 * s, 1);
+        }
+        for (int s = 0; s < 2; ++s) mbar_init(bar_of + 8 * s, 1);  // per pair: each sees every other output
+        mbar_init(bar_oe, kSoftWarps / 2);
         mbar_init(bar_dr, 1);
         misc[1] = 0;
         fence_barrier_init();
@@ -182,7 +197,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
         tmem_alloc(smem_u32((const void *)&misc[0]), 512);
         tmem_relinquish();
         tc_fence_before();
-        named_bar_sync(2, NS + 32);
+        named_bar_sync(5, NS + 32);
         tc_fence_after();
         const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
         constexpr uint32_t kIdS = idesc_i8(128, kStep);
@@ -192,24 +207,24 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             return (bool)__all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(parity & 1), lim.wait_ns, abort_flag));
         };
         bool ok = true;
-        int qn = 0, kn = 0, k0 = 0, vn = 0, pn = 0, on = 0;  // kn: K tiles whose scores, k0: whose products are done
-        uint32_t ef_par = 0;
+        int qn = 0, kn = 0, k0 = 0, vn = 0, sn = 0, pn = 0, on = 0;  // kn, sn: K tiles, steps whose scores, k0, pn: whose products are issued
         for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
             const AttnItem w = attn_item(a, item);
             if (w.nt == 0) continue;
             const int nu = (w.most + kStep - 1) / kStep;
             const uint32_t qt = sb + (qn % L::QS) * 2 * L::kTile;
             if (!(ok = wait(bar_qf + 8 * (qn % L::QS), qn / L::QS))) break;
-            // S and dP of step u into buffer u & 1
+            // S and dP of the item's step u; the buffer's last T planes (NB steps ago) are used
             auto scores = [&](int u) {
-                const int s = kn % L::KS, v = vn % L::VS, half = u & 1;
+                const int s = kn % L::KS, v = vn % L::VS, half = u & 1, buf = sn % L::NB;
+                if (sn >= L::NB && !wait(bar_ee + 8 * buf, sn / L::NB - 1)) return false;
                 if (half == 0 && (!wait(bar_kf + 8 * s, kn / L::KS) || !wait(bar_vf + 8 * v, vn / L::VS))) return false;
                 tc_fence_after();
                 const bool done = half == 1 || u + 1 == nu;
                 const uint64_t dq = smem_desc_kmajor(qt, 64), dd = smem_desc_kmajor(qt + L::kTile, 64);
                 const uint64_t dk = smem_desc_kmajor(sb + L::kOffK + s * L::kTile + half * kStep * 64, 64);
                 const uint64_t dv = smem_desc_kmajor(sb + L::kOffV + v * L::kTile + half * kStep * 64, 64);
-                const uint32_t col = tm + (u & 1) * 128;
+                const uint32_t col = tm + buf * 128;
                 if (elect_one()) {
 #pragma unroll
                     for (int x = 0; x < 2 * H; ++x) {
@@ -223,38 +238,34 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
                     }
                     if (done) umma_commit(bar_ve + 8 * v);
                     if (u + 1 == nu) umma_commit(bar_qe + 8 * (qn % L::QS));
-                    umma_commit(bar_sf + 8 * (u & 1));
+                    umma_commit(bar_sf + 8 * buf);
                 }
                 __syncwarp();
+                ++sn;
                 if (done) ++kn, ++vn;
                 return true;
             };
-            // the last item's T planes are used; its dQ is read before this item's first product
-            if (pn > 0 && !(ok = wait(bar_ee, pn - 1))) break;
-            ok = scores(0);
+            for (int u = 0; u < L::NB - 1 && u < nu && ok; ++u) ok = scores(u);
             for (int u = 0; u < nu && ok; ++u) {
-                if (u + 1 < nu) {
-                    if (u > 0) ok = wait(bar_ee, pn - 1);
-                    if (!ok || !(ok = scores(u + 1))) break;
-                }
-                if (!(ok = wait(bar_ef + 8 * (u & 1), (ef_par >> (u & 1)) & 1))) break;
-                ef_par ^= 1u << (u & 1);
-                if (u == 0 && on > 0 && !(ok = wait(bar_oe, on - 1))) break;
+                if (u + L::NB - 1 < nu && !(ok = scores(u + L::NB - 1))) break;
+                const int buf = pn % L::NB;
+                if (!(ok = wait(bar_ef + 8 * buf, pn / L::NB))) break;
+                if (u == 0 && on > 0 && !(ok = wait(bar_oe, on - 1))) break;  // the last item's dQ is read
                 tc_fence_after();
                 const int s = k0 % L::KS, ks = (min(kStep, w.most - u * kStep) + 31) / 32;
                 const uint64_t dk = smem_desc_mnmajor64(sb + L::kOffK + s * L::kTile + (u & 1) * kStep * 64, kHalfTile);
-                const uint32_t e0 = tm + (u & 1) * 128, first = u ? 1u : 0u;
+                const uint32_t e0 = tm + buf * 128, first = u ? 1u : 0u;
                 const bool done = (u & 1) || u + 1 == nu;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk)
                         if (kk < ks) {
-                            umma_i8_ta(tm + kAccCol, e0 + kk * 32, dk + 128 * kk, kIdHi, kk ? 1u : first);
-                            umma_i8_ta(tm + kAccCol + DP, e0 + kk * 32 + 8, dk + 128 * kk, kIdLo, kk ? 1u : first);
+                            umma_i8_ta(tm + L::kAcc, e0 + kk * 32, dk + 128 * kk, kIdHi, kk ? 1u : first);
+                            umma_i8_ta(tm + L::kAcc + DP, e0 + kk * 32 + 8, dk + 128 * kk, kIdLo, kk ? 1u : first);
                         }
                     if (done) umma_commit(bar_ke + 8 * s);
-                    umma_commit(bar_ee);
-                    if (u + 1 == nu) umma_commit(bar_of);
+                    umma_commit(bar_ee + 8 * buf);
+                    if (u + 1 == nu) umma_commit(bar_of + 8 * (on & 1));
                 }
                 __syncwarp();
                 ++pn;
@@ -269,14 +280,13 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
         wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
     } else {
         // ------------------------------------------------------------ softmax
-        named_bar_sync(2, NS + 32);
+        named_bar_sync(5, NS + 32);
         tc_fence_after();
         const uint32_t tm = (uint32_t)misc[0];
         const int wg = warp >> 2, et = threadIdx.x & 127, pair = wg >> 1, c0 = (wg & 1) * 32;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        int *red = (int *)(smem + L::kOffRed + 8 * 128 * 8);
         bool ok = true;
-        int on = 0, sn = 0;  // outputs, this pair's steps so far
+        int on = 0, gn = 0;  // outputs, steps of the items so far
         for (int item = blockIdx.x; item < items; item += gridDim.x) {  // (outputs are written after a failure too)
             const AttnItem w = attn_item(a, item);
             const int i = w.i0 + et, nu = (w.most + kStep - 1) / kStep, bg = w.b * a.Hkv + w.g;
@@ -290,14 +300,14 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             const f2 nm = pk(-(kAttnMagic + (float)st.x)), nd = pk(-(kAttnMagic + (float)rw.x));
             const f2 f = pk(attn_factor(a, bg)), sc = pk(pow2f(-tau));
             int tmax = 0x4B400000, tmin = 0x4B400000;
-            for (int u = pair; u < nu && ok; u += 2) {
-                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, sn & 1, lim.wait_ns, abort_flag));
+            for (int u = (pair ^ gn) & 1; u < nu && ok; u += 2) {
+                const int buf = (gn + u) % L::NB;
+                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * buf, ((gn + u) / L::NB) & 1, lim.wait_ns, abort_flag));
                 if (!ok) break;
-                ++sn;
                 tc_fence_after();
                 const int col = u * kStep + c0;
                 if (c0 < w.most - u * kStep) {
-                    const uint32_t mine = tm + lanes + pair * 128 + c0;
+                    const uint32_t mine = tm + lanes + buf * 128 + c0;
 #pragma unroll 1
                     for (int c = 0; c < 32; c += 16) {
                         uint32_t lo[4] = {0, 0, 0, 0}, hi[4] = {0, 0, 0, 0};
@@ -314,24 +324,33 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
                     }
                     tmem_st_wait();
                 }
-                warp_arrive(bar_ef + 8 * pair);
+                warp_arrive(bar_ef + 8 * buf);
             }
+            gn += nu;
+            if (w.nt == 0) {
+                if (pair == 0 && live) zero_row(a, a.o, (int64_t)w.b * a.Lq + i, w.h, (wg & 1) * (DP / 2), DP / 2);
+                if (wg == 0 && live) a.tmax[at] = 0;
+                continue;
+            }
+            // the item's output is this turn's pair's; the other leaves its maxima and goes on
+            const int turn = on & 1;
+            int *red = (int *)(smem + L::kOffRed + 2 * 8 * 128 * 8) + turn * 4 * 128;
             red[wg * 128 + et] = max(tmax - 0x4B400000, 0x4B400000 - tmin);
-            if (w.nt > 0 && ok) {
-                ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
-                tc_fence_after();
-            }
-            const bool read = w.nt > 0 && ok;
-            float2 *gm = (float2 *)(smem + L::kOffRed) + et;
-            fit_row_tmem<DP / 64>(a, a.o, (int64_t)w.b * a.Lq + i, w.h, wg * (DP / 4), read ? st.y : 0, a.mul,
-                                  tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
-                                  w.nk <= 1024, gm, 128, 1, NS, AccCols{tm + lanes + kAccCol, DP, read});
-            if (wg == 0 && live) a.tmax[at] = max(max(red[et], red[128 + et]), max(red[256 + et], red[384 + et]));
-            if (w.nt > 0) {
-                warp_arrive(bar_oe);
+            if (pair != turn) {
+                named_bar_arrive(3 + turn, NS);
                 ++on;
+                continue;
             }
-            named_bar_sync(1, NS);  // the shared maxima are read before the next item's are written
+            named_bar_sync(3 + turn, NS);
+            if (wg == 2 * turn && live) a.tmax[at] = max(max(red[et], red[128 + et]), max(red[256 + et], red[384 + et]));
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of + 8 * turn, (on >> 1) & 1, lim.wait_ns, abort_flag));
+            tc_fence_after();
+            float2 *gm = (float2 *)(smem + L::kOffRed) + turn * 8 * 128 + et;
+            fit_row_tmem<DP / 32>(a, a.o, (int64_t)w.b * a.Lq + i, w.h, (wg & 1) * (DP / 2), ok ? st.y : 0, a.mul,
+                                  tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
+                                  w.nk <= 1024, gm, 128, 1 + turn, NS / 2, AccCols{tm + lanes + L::kAcc, DP, ok});
+            warp_arrive(bar_oe);
+            ++on;
         }
         if (!ok && lane == 0) fail();
     }
@@ -353,9 +372,9 @@ struct DkvCfg {
     static constexpr int H = DP / 64, kTile = H * kHalfTile, KS = 2, QS = 2;
     static constexpr int kOffQ = KS * 2 * kTile;                           // K stage: K tile, V tile; Q stage: Q tile, dO tile
     static constexpr int kOffVec = kOffQ + QS * 2 * kTile;                 // [4][3][64] floats
-    static constexpr int kOffRed = kOffVec + 4 * 3 * kStep * 4;            // [2][8][128] float2
+    static constexpr int kOffRed = kOffVec + 4 * 3 * kStep * 4;            // [4][4][128] float2
     static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8;
-    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 2 + 2 + 4;
+    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 2 + 2 + 6;
     static constexpr int kBytes = kOffBar + kBars * 8 + 64 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 96;
 };
@@ -401,7 +420,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
     const uint32_t bar_sf = bar_qe + 8 * L::QS, bar_ef = bar_sf + 16;
     const uint32_t bar_cf = bar_ef + 16, bar_ce = bar_cf + 32;  // the queries' vectors full / empty
     const uint32_t bar_xf = bar_ce + 32, bar_xe = bar_xf + 16;  // an item's exponents full / empty
-    const uint32_t bar_ee = bar_xe + 16, bar_of = bar_ee + 8, bar_oe = bar_of + 8, bar_dr = bar_oe + 8;
+    const uint32_t bar_ee = bar_xe + 16, bar_of = bar_ee + 16, bar_oe = bar_of + 16, bar_dr = bar_oe + 8;
     // tmem, abort, -, -, [2] pi, c, [2] smallest sum, [2] largest bound (64 bits)
     volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);
     int *smin = (int *)(misc + 8);
@@ -419,12 +438,12 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             mbar_init(bar_sf + 8 * s, 1);
             mbar_init(bar_ef + 8 * s, kSoftWarps / 2);
             mbar_init(bar_xf + 8 * s, 1);
+            mbar_init(bar_ee + 8 * s, 1);
             mbar_init(bar_xe + 8 * s, kSoftWarps);
         }
         for (int s = 0; s < 4; ++s) mbar_init(bar_cf + 8 * s, 1), mbar_init(bar_ce + 8 * s, kSoftWarps / 2);
-        mbar_init(bar_ee, 1);
-        mbar_init(bar_of, 1);
-        mbar_init(bar_oe, kSoftWarps);
+        for (int s = 0; s < 2; ++s) mbar_init(bar_of + 8 * s, 1);  // per pair: each sees every other output
+        mbar_init(bar_oe, kSoftWarps / 2);
         mbar_init(bar_dr, 1);
         misc[1] = 0;
         smin[0] = smin[1] = INT_MAX;
@@ -516,7 +535,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         tmem_alloc(smem_u32((const void *)&misc[0]), 512);
         tmem_relinquish();
         tc_fence_before();
-        named_bar_sync(3, NS + 32);
+        named_bar_sync(5, NS + 32);
         tc_fence_after();
         const uint32_t tm = __shfl_sync(0xffffffffu, (uint32_t)misc[0], 0);
         constexpr uint32_t kIdS = idesc_i8(128, kStep);
@@ -528,7 +547,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         };
         bool ok = true;
         int kn = 0, pn = 0, on = 0, sw = 0, pw = 0;  // sw, pw: query tiles whose scores, products are done
-        uint32_t ef_par = 0;
+        int sn = 0;  // steps whose scores are issued (step G of all items in buffer G & 1)
         for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
             const KeyItem w = key_item(a, item);
             if (w.nu == 0) continue;
@@ -537,13 +556,14 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             // half within the tile and step within the head, for the scores and for the products
             int sh = 0, sk = 0, ph = 0, pk_ = 0;
             auto scores = [&](int u) {
-                const int s = sw % L::QS;
+                const int s = sw % L::QS, buf = sn & 1;
+                if (sn >= 2 && !wait(bar_ee + 8 * buf, (sn >> 1) - 1)) return false;  // the buffer's last planes are used
                 if (sh == 0 && !wait(bar_qf + 8 * s, sw / L::QS)) return false;
                 tc_fence_after();
                 const uint32_t q = sb + L::kOffQ + s * 2 * L::kTile + sh * kStep * 64;
                 const uint64_t dk = smem_desc_kmajor(kt, 64), dv = smem_desc_kmajor(kt + L::kTile, 64);
                 const uint64_t dq = smem_desc_kmajor(q, 64), dd = smem_desc_kmajor(q + L::kTile, 64);
-                const uint32_t col = tm + (u & 1) * 128;
+                const uint32_t col = tm + buf * 128;
                 if (elect_one()) {
 #pragma unroll
                     for (int x = 0; x < 2 * H; ++x) {
@@ -558,28 +578,25 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                         }
                     }
                     if (u + 1 == w.nu) umma_commit(bar_ke + 8 * (kn % L::KS));
-                    umma_commit(bar_sf + 8 * (u & 1));
+                    umma_commit(bar_sf + 8 * buf);
                 }
                 __syncwarp();
+                ++sn;
                 if (++sk == w.per) sk = 0, sh = 0, ++sw;
                 else if ((sh ^= 1) == 0) ++sw;
                 return true;
             };
-            if (pn > 0 && !(ok = wait(bar_ee, pn - 1))) break;
             ok = scores(0);
             for (int u = 0; u < w.nu && ok; ++u) {
-                if (u + 1 < w.nu) {
-                    if (u > 0) ok = wait(bar_ee, pn - 1);
-                    if (!ok || !(ok = scores(u + 1))) break;
-                }
-                if (!(ok = wait(bar_ef + 8 * (u & 1), (ef_par >> (u & 1)) & 1))) break;
-                ef_par ^= 1u << (u & 1);
+                if (u + 1 < w.nu && !(ok = scores(u + 1))) break;
+                const int buf = pn & 1;
+                if (!(ok = wait(bar_ef + 8 * buf, pn >> 1))) break;
                 if (u == 0 && on > 0 && !(ok = wait(bar_oe, on - 1))) break;  // the last item's gradients are read
                 tc_fence_after();
                 const int s = pw % L::QS;
                 const uint32_t q = sb + L::kOffQ + s * 2 * L::kTile + ph * kStep * 64;
                 const uint64_t dq = smem_desc_mnmajor64(q, kHalfTile), dd = smem_desc_mnmajor64(q + L::kTile, kHalfTile);
-                const uint32_t e0 = tm + (u & 1) * 128, first = u ? 1u : 0u;
+                const uint32_t e0 = tm + buf * 128, first = u ? 1u : 0u;
                 const bool done = pk_ + 1 == w.per || ph == 1;
                 if (elect_one()) {
 #pragma unroll
@@ -594,8 +611,8 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                         }
                     }
                     if (done) umma_commit(bar_qe + 8 * s);
-                    umma_commit(bar_ee);
-                    if (u + 1 == w.nu) umma_commit(bar_of);
+                    umma_commit(bar_ee + 8 * buf);
+                    if (u + 1 == w.nu) umma_commit(bar_of + 8 * (on & 1));
                 }
                 __syncwarp();
                 ++pn;
@@ -695,13 +712,13 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         if (!ok && lane == 0) fail();
     } else {
         // ------------------------------------------------------------ softmax: lane = key
-        named_bar_sync(3, NS + 32);
+        named_bar_sync(5, NS + 32);
         tc_fence_after();
         const uint32_t tm = (uint32_t)misc[0];
         const int wg = warp >> 2, et = threadIdx.x & 127, pair = wg >> 1, c0 = (wg & 1) * 32;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
-        int on = 0, sn = 0, xn = 0, ln = 0, cn = 0;  // outputs, this pair's steps, items of few and of many queries, all steps
+        int on = 0, xn = 0, ln = 0, cn = 0;  // outputs, items of few and of many queries, steps of the items so far
         for (int item = blockIdx.x; item < items; item += gridDim.x) {  // (outputs are written after a failure too)
             const KeyItem w = key_item(a, item);
             const int j = w.j0 + et;
@@ -719,17 +736,17 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const f2 f = pk(attn_factor(a, w.bg)), sc = pk(pow2f(-cexp));
             const int lo_i = a.causal ? j - w.off : 0;  // the first query that sees this key
             const int lo_max = warp_max(lo_i);
-            int k_in = w.per > 0 ? pair % w.per : 0;
-            for (int u = pair; u < w.nu && ok; u += 2) {
-                const int cs = (cn + u) & 3;
-                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * pair, sn & 1, lim.wait_ns, abort_flag) &&
+            const int u0 = (pair ^ cn) & 1;
+            int k_in = w.per > 0 ? u0 % w.per : 0;
+            for (int u = u0; u < w.nu && ok; u += 2) {
+                const int cs = (cn + u) & 3, buf = (cn + u) & 1;
+                ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * buf, ((cn + u) >> 1) & 1, lim.wait_ns, abort_flag) &&
                                                  wait_bar(bar_cf + 8 * cs, ((cn + u) >> 2) & 1, lim.wait_ns, abort_flag));
                 if (!ok) break;
-                ++sn;
                 tc_fence_after();
                 const float *vec = (const float *)(smem + L::kOffVec) + cs * 3 * kStep + c0;
                 const int i = w.base + k_in * kStep + c0;
-                const uint32_t mine = tm + lanes + pair * 128 + c0;
+                const uint32_t mine = tm + lanes + buf * 128 + c0;
 #pragma unroll 1
                 for (int c = 0; c < 32; c += 16) {
                     uint32_t vs[16], vd[16], plo[4], phi[4], ulo[4], uhi[4];
@@ -750,32 +767,35 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                     }
                 }
                 tmem_st_wait();
-                warp_arrive(bar_ef + 8 * pair);
+                warp_arrive(bar_ef + 8 * buf);
                 if (lane == 0) mbar_arrive(bar_ce + 8 * cs);
                 if ((k_in += 2) >= w.per) k_in %= w.per;
             }
             cn += w.nu;
-            if (w.nu > 0 && ok) {
-                ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
-                tc_fence_after();
+            const bool live = j < a.Lk;
+            const int64_t row = (int64_t)w.b * a.Lk + j;
+            if (w.nu == 0) {
+                if (pair == 0 && live) {
+                    if ((MODE & 1) && (wg == 0 || MODE != 3)) zero_row(a, a.dv, row, w.g, MODE == 3 ? 0 : wg * 64, 64);
+                    if ((MODE & 2) && (wg == 1 || MODE != 3)) zero_row(a, a.dk, row, w.g, MODE == 3 ? 0 : wg * 64, 64);
+                }
+                continue;
             }
-            const bool live = j < a.Lk, read = w.nu > 0 && ok;
+            const int turn = on & 1;  // the item's outputs are this turn's pair's; the other goes on
+            ++on;
+            if (pair != turn) continue;
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of + 8 * turn, ((on - 1) >> 1) & 1, lim.wait_ns, abort_flag));
+            tc_fence_after();
             const int ed = attn_top(a, OPD, w.bg), ev = attn_top(a, OPV, w.bg), eq = attn_top(a, OPQ, w.bg);
-            // 32 columns of one gradient per warpgroup
-            const bool is_k = MODE == 3 ? wg >= 2 : MODE == 2;
-            const int cc = MODE == 3 ? (wg & 1) * 32 : wg * 32, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
-            float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 8 * 128 : 0) + et;
-            const int den = read && j < w.nk ? 1 : 0;
-            const bool narrow = (int64_t)w.nq * a.rep <= 1024;
-            const int bar = MODE == 3 ? 1 + (wg >> 1) : 1, nthr = MODE == 3 ? NS / 2 : NS;
-            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, (int64_t)w.b * a.Lk + j, w.g, cc, den, is_k ? a.mul : 1,
-                            is_k ? cexp - pi - a.shift + ed + ev + eq : ed - pi, live, narrow, gm, 128, bar, nthr,
-                            AccCols{tm + lanes + acc, DP, read});
-            if (w.nu > 0) {
-                warp_arrive(bar_oe);
-                ++on;
-            }
-            named_bar_sync(bar, nthr);  // the shared maxima are read before the next item's are written
+            // 64 columns of one gradient per warpgroup
+            const bool is_k = MODE == 3 ? (wg & 1) == 1 : MODE == 2;
+            const int cc = MODE == 3 ? 0 : (wg & 1) * 64, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
+            float2 *gm = (float2 *)(smem + L::kOffRed) + (turn * 2 + (MODE == 3 ? wg & 1 : 0)) * 4 * 128 + et;
+            const int den = ok && j < w.nk ? 1 : 0;
+            fit_row_tmem<4>(a, is_k ? a.dk : a.dv, row, w.g, cc, den, is_k ? a.mul : 1,
+                            is_k ? cexp - pi - a.shift + ed + ev + eq : ed - pi, live, (int64_t)w.nq * a.rep <= 1024, gm, 128,
+                            MODE == 3 ? 6 + wg : 1 + turn, MODE == 3 ? 128 : NS / 2, AccCols{tm + lanes + acc, DP, ok});
+            warp_arrive(bar_oe);
         }
         if (!ok && lane == 0) fail();
     }
