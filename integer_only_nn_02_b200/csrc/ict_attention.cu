@@ -203,6 +203,15 @@ int check_out(const ict_tensor *t, int64_t rows, int col, int64_t width, int D) 
     return ICT_OK;
 }
 
+// Few key blocks leave SMs without work, and causal ones differ in length: their queries are then
+// shared by up to kSplitTarget / blocks parts of at least kSplitTiles tiles.
+constexpr int kSplitTarget = 4 * 148, kSplitTiles = 4;
+int split_parts(const AttnArgs &a) {
+    if (a.blocks == 0) return 1;
+    const int64_t tiles = host::cdiv(a.Lq, 128) * a.rep;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kSplitTarget / a.blocks, tiles / kSplitTiles));
+}
+
 int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
     if (!d) return ICT_ERR_INVALID_ARG;
     if (d->batch < 0 || d->heads_q < 1 || d->heads_kv < 1 || d->len_q < 0 || d->len_k < 0 || d->head_dim < 1 ||
@@ -220,6 +229,8 @@ int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
     a.D = d->head_dim, a.Dp = a.D <= 64 ? 64 : 128, a.causal = d->causal, a.mul = d->scale_mul, a.shift = d->scale_shift;
     a.fmul = (float)((double)d->scale_mul * 12102203.0);  // log2(e) 2^23
     a.n_op = back ? 4 : 3;
+    a.blocks = (int)(host::cdiv(a.Lk, kKeyBlock) * a.B * a.Hkv);
+    a.parts = back ? split_parts(a) : 1;
     return ICT_OK;
 }
 
@@ -234,6 +245,7 @@ bool few_queries_path(const AttnArgs &a, bool back) {
 struct Scratch {
     size_t top, copy[OPN], row, tmax, total;
     size_t scores, mx, sum, acc;  // the few-queries path (scores apart, the others cleared before use)
+    size_t exps, join, tickets;   // backward (tickets and join are cleared before use)
 };
 Scratch scratch(const AttnArgs &a, bool back) {
     Scratch s = {};
@@ -260,6 +272,12 @@ Scratch scratch(const AttnArgs &a, bool back) {
     s.copy[OPD] = take(back ? q * a.Dp : 0);
     s.row = take(back ? q * 8 : 0);
     s.tmax = take(back ? q * 4 : 0);
+    s.exps = take(back ? (int64_t)a.blocks * 8 : 0);
+    if (back && a.parts > 1) {
+        const int64_t n = (int64_t)a.blocks * (a.Dp / 64);
+        s.tickets = take(n * 4);
+        s.join = take(n * 256 * 128 * 4);
+    }
     s.total = at;
     return s;
 }
@@ -403,8 +421,16 @@ int launch_bwd(const AttnArgs &a, cudaStream_t s) {
     }
     if ((int64_t)a.B * a.Lk > 0) {
         using L = DkvCfg<DP>;
-        const int64_t items = host::cdiv(a.Lk, kKeyBlock) * a.B * a.Hkv;
+        const int64_t items = (int64_t)a.blocks * a.parts;
         const unsigned blocks = blocks_for(items, 1, a.Lq * a.rep);
+        const unsigned threads = (unsigned)std::min<int64_t>(1024, host::round_up((int64_t)a.Lq * a.rep / 2 + 1, 64));
+        attn_exps_kernel<<<(unsigned)a.blocks, threads, 0, s>>>(a);
+        host::counted(1);
+        if (a.parts > 1) {
+            const int64_t n = (int64_t)a.blocks * (DP / 64);
+            if (cudaMemsetAsync(a.tickets, 0, (size_t)((uint8_t *)(a.join + n * 256 * 128) - (uint8_t *)a.tickets), s) != cudaSuccess)
+                return ICT_ERR_CUDA;
+        }
         if constexpr (DP == 64) {
             if ((st = allow_smem(attn_dkv_kernel<64, 3>, L::kBytes))) return st;
             attn_dkv_kernel<64, 3><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
@@ -484,6 +510,8 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     output(a.dv, dV, d->v_col);
     a.row = (int2 *)(base + w.row);
     a.tmax = (int32_t *)(base + w.tmax);
+    a.exps = (int2 *)(base + w.exps);
+    if (a.parts > 1) a.tickets = (int32_t *)(base + w.tickets), a.join = (int32_t *)(base + w.join);
     if (rq == 0 && rk == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t rows = rq * a.Hq;

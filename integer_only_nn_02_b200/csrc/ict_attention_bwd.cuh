@@ -371,25 +371,28 @@ template <int DP>
 struct DkvCfg {
     static constexpr int H = DP / 64, kTile = H * kHalfTile, KS = 2, QS = 2;
     static constexpr int kOffQ = KS * 2 * kTile;                           // K stage: K tile, V tile; Q stage: Q tile, dO tile
-    static constexpr int kOffVec = kOffQ + QS * 2 * kTile;                 // [4][3][64] floats
-    static constexpr int kOffRed = kOffVec + 4 * 3 * kStep * 4;            // [4][4][128] float2
+    static constexpr int kVec = 3 * kStep + 4;                             // a step's floats: see dkv16, then f and 2^-c
+    static constexpr int kOffVec = kOffQ + QS * 2 * kTile;                 // [4][kVec] floats
+    static constexpr int kOffRed = kOffVec + 4 * kVec * 4;                 // [4][4][128] float2
     static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8;
-    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 2 + 2 + 6;
-    static constexpr int kBytes = kOffBar + kBars * 8 + 64 + 1024;
+    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 6;
+    static constexpr int kBytes = kOffBar + kBars * 8 + 16 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 96;
 };
 
-// One work item: a block of keys of one key/value head.  Heavy causal blocks come first.
+// One work item: a block of keys of one key/value head, or a part of the queries that see it (tiles
+// of 128 queries, head after head).  Heavy causal blocks come first.
 struct KeyItem {
-    int b, g, bg, j0, nq, nk, off, i0, n, base, tiles, per, nw, nu;
+    int b, g, bg, j0, nq, nk, off, i0, n, base, tiles, per, slot, join, t0, nw, u0, nu;
 };
 __device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
     KeyItem w;
-    const int heads = a.B * a.Hkv, J = item / heads;
-    w.bg = item - J * heads;
+    const int heads = a.B * a.Hkv, J = item / (heads * a.parts), r = item - J * heads * a.parts, part = r / heads;
+    w.bg = r - part * heads;
     w.b = w.bg / a.Hkv;
     w.g = w.bg - w.b * a.Hkv;
     w.j0 = J * kKeyBlock;
+    w.slot = J * heads + w.bg;
     w.nq = clamp_len(a.op[OPQ].lens, w.b, a.Lq);
     w.nk = clamp_len(a.op[OPK].lens, w.b, a.Lk);
     w.off = w.nk - w.nq;
@@ -398,9 +401,94 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
     w.base = w.i0 & ~(kStep - 1);
     w.tiles = w.n > 0 ? (w.nq - w.base + 127) / 128 : 0;
     w.per = w.n > 0 ? (w.nq - w.base + kStep - 1) / kStep : 0;  // steps of one head
-    w.nw = w.tiles * a.rep;
-    w.nu = w.per * a.rep;
+    const int all = w.tiles * a.rep;
+    w.join = min(a.parts, max(all, 1));  // parts with work (one for a block that no query sees)
+    w.t0 = w.nw = w.u0 = w.nu = 0;
+    if (part < w.join && all > 0) {
+        const int t1 = all * (part + 1) / w.join;
+        w.t0 = all * part / w.join;
+        w.nw = t1 - w.t0;
+        w.u0 = (w.t0 / w.tiles) * w.per + 2 * (w.t0 % w.tiles);
+        w.nu = (t1 / w.tiles) * w.per + 2 * (t1 % w.tiles) - w.u0;
+    } else if (part >= w.join) {
+        w.join = 0;  // nothing to do
+    }
     return w;
+}
+
+// The exponents of every key block: pi from the smallest sum of weights, c from the largest bound,
+// over the queries that see the block.  One block of threads each, of up to 1024.
+__global__ void __launch_bounds__(1024) attn_exps_kernel(const __grid_constant__ AttnArgs a) {
+    __shared__ int smin;
+    __shared__ unsigned long long bmax;
+    const int heads = a.B * a.Hkv, J = blockIdx.x / heads, bg = blockIdx.x - J * heads, b = bg / a.Hkv;
+    const int nq = clamp_len(a.op[OPQ].lens, b, a.Lq), nk = clamp_len(a.op[OPK].lens, b, a.Lk), j0 = J * kKeyBlock;
+    const int i0 = j0 < nk ? (a.causal ? max(0, j0 - (nk - nq)) : 0) : nq, n = nq - i0, total = n > 0 ? n * a.rep : 0;
+    const int64_t head0 = (int64_t)bg * a.rep * a.Lq + i0;
+    auto row = [&](int t) {
+        const int r = t / n;
+        return head0 + (int64_t)r * a.Lq + (t - r * n);
+    };
+    if (threadIdx.x == 0) smin = INT_MAX, bmax = 0;
+    __syncthreads();
+    int m = INT_MAX;
+#pragma unroll 4
+    for (int t = threadIdx.x; t < total; t += blockDim.x) {
+        const int S = a.stats[row(t)].y;
+        m = S > 0 ? min(m, S) : m;
+    }
+    m = -warp_max(-m);
+    if ((threadIdx.x & 31) == 0) atomicMin(&smin, m);
+    __syncthreads();
+    m = smin;
+    const int pi = m == INT_MAX ? 0 : 31 - __clz(m);
+    unsigned long long x = 0;
+#pragma unroll 4
+    for (int t = threadIdx.x; t < total; t += blockDim.x) {
+        const int64_t at = row(t);
+        const int S = a.stats[at].y, tmax = a.tmax[at], X = a.row[at].y;
+        if (S > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), tmax, X));
+    }
+    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    if ((threadIdx.x & 31) == 0) atomicMax(&bmax, x);
+    __syncthreads();
+    if (threadIdx.x == 0) a.exps[blockIdx.x] = make_int2(pi, max(0, 64 - __clzll((long long)bmax) - 14));
+}
+
+// A part's sums join the other parts' in memory: 32-bit integers, so that their order does not
+// matter.  The last part to come (true) takes the totals back into its accumulators.  sums: this
+// thread's row of [columns][128 keys] (high planes' 64 columns; low planes lo_cols further on).
+__device__ __noinline__ bool join_parts(const AccCols acc, int c0, int32_t *sums, int lo_cols, int *tickets, int join,
+                                        volatile int *shared, int bar, int nthreads) {
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 16) {
+        uint32_t hi[16], lo[16];
+        acc.load16(c0 + c, hi, lo);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            atomicAdd(sums + (c + q) * 128, (int)hi[q]);
+            atomicAdd(sums + (lo_cols + c + q) * 128, (int)lo[q]);
+        }
+    }
+    __threadfence();
+    named_bar_sync(bar, nthreads);
+    if (tickets) *shared = atomicAdd(tickets, 1);
+    named_bar_sync(bar, nthreads);
+    if (*shared != join - 1) return false;
+    __threadfence();
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 4) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            hi[q] = (uint32_t)__ldcg(sums + (c + q) * 128);
+            lo[q] = (uint32_t)__ldcg(sums + (lo_cols + c + q) * 128);
+        }
+        tmem_st4(acc.hi + c0 + c, hi);
+        tmem_st4(acc.hi + acc.lo + c0 + c, lo);
+    }
+    tmem_st_wait();
+    return true;
 }
 
 // MODE: 3 computes dV and dK (heads of 64 columns), 1 only dV, 2 only dK.  Persistent blocks.
@@ -419,12 +507,8 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
     const uint32_t bar_qf = bar_ke + 8 * L::KS, bar_qe = bar_qf + 8 * L::QS;
     const uint32_t bar_sf = bar_qe + 8 * L::QS, bar_ef = bar_sf + 16;
     const uint32_t bar_cf = bar_ef + 16, bar_ce = bar_cf + 32;  // the queries' vectors full / empty
-    const uint32_t bar_xf = bar_ce + 32, bar_xe = bar_xf + 16;  // an item's exponents full / empty
-    const uint32_t bar_ee = bar_xe + 16, bar_of = bar_ee + 16, bar_oe = bar_of + 16, bar_dr = bar_oe + 8;
-    // tmem, abort, -, -, [2] pi, c, [2] smallest sum, [2] largest bound (64 bits)
-    volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);
-    int *smin = (int *)(misc + 8);
-    unsigned long long *bmax = (unsigned long long *)(misc + 10);
+    const uint32_t bar_ee = bar_ce + 32, bar_of = bar_ee + 16, bar_oe = bar_of + 16, bar_dr = bar_oe + 8;
+    volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);  // tmem, abort, a ticket per pair
     volatile int *abort_flag = &misc[1];
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == NS) {
@@ -437,17 +521,13 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         for (int s = 0; s < 2; ++s) {
             mbar_init(bar_sf + 8 * s, 1);
             mbar_init(bar_ef + 8 * s, kSoftWarps / 2);
-            mbar_init(bar_xf + 8 * s, 1);
             mbar_init(bar_ee + 8 * s, 1);
-            mbar_init(bar_xe + 8 * s, kSoftWarps);
         }
         for (int s = 0; s < 4; ++s) mbar_init(bar_cf + 8 * s, 1), mbar_init(bar_ce + 8 * s, kSoftWarps / 2);
         for (int s = 0; s < 2; ++s) mbar_init(bar_of + 8 * s, 1);  // per pair: each sees every other output
         mbar_init(bar_oe, kSoftWarps / 2);
         mbar_init(bar_dr, 1);
         misc[1] = 0;
-        smin[0] = smin[1] = INT_MAX;
-        bmax[0] = bmax[1] = 0;
         fence_barrier_init();
     }
     __syncthreads();
@@ -455,45 +535,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         *abort_flag = 1;
         raise_status(ICT_ERR_DEVICE_TIMEOUT);
     };
-    // An item's exponents: pi from the smallest sum of weights, c from the largest bound, over the
-    // queries that see the block.  Few queries: the vector warp finds them, an item ahead.  Many:
-    // the softmax warps do, all their threads reading; both then meet at a barrier (slot ls of
-    // the two alternates; thread 0 clears the other one, whose readers have passed a barrier).
-    auto row_of = [&](const KeyItem &w, int t) {
-        const int r = t / w.n;
-        return ((int64_t)w.b * a.Hq + w.g * a.rep + r) * a.Lq + w.nq - w.n + (t - r * w.n);
-    };
-    auto is_long = [&](const KeyItem &w) { return w.n * a.rep > 512; };
-    auto long_exponents = [&](const KeyItem &w, int ls, int tid, int &pi, int &c) {  // tid < 0: only meet
-        const int total = w.n * a.rep;
-        if (tid >= 0) {
-            int m = INT_MAX;
-            for (int t = tid; t < total; t += NS) {
-                const int S = a.stats[row_of(w, t)].y;
-                m = S > 0 ? min(m, S) : m;
-            }
-            m = -warp_max(-m);
-            if (lane == 0) atomicMin(&smin[ls], m);
-        }
-        named_bar_sync(4, NS + 32);
-        const int m = *(volatile int *)&smin[ls];
-        pi = m == INT_MAX ? 0 : 31 - __clz(m);
-        if (tid == 0) smin[ls ^ 1] = INT_MAX, bmax[ls ^ 1] = 0;
-        if (tid >= 0 && (MODE & 2)) {
-            unsigned long long x = 0;
-            for (int t = tid; t < total; t += NS) {
-                const int64_t at = row_of(w, t);
-                const int S = a.stats[at].y;
-                if (S > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), a.tmax[at], a.row[at].y));
-            }
-            for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-            if (lane == 0) atomicMax(&bmax[ls], x);
-        }
-        named_bar_sync(4, NS + 32);
-        const unsigned long long x = *(volatile unsigned long long *)&bmax[ls];
-        c = max(0, 64 - __clzll((long long)x) - 14);
-    };
-    // step u of an item: query head g rep + u / per, queries base + (u % per) 64 ...
+    // step u of a key block (an item has nu from u0 on): query head g rep + u / per, queries base + (u % per) 64 ...
     if (warp == kSoftWarps) {
         // ------------------------------------------------------------ TMA producer
         if (lane == 0) {
@@ -514,7 +556,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 load_tile(&tmK, dst, bar, w.bg * a.Lk + w.j0);
                 load_tile(&tmV, dst + L::kTile, bar, w.bg * a.Lk + w.j0);
                 ++kn;
-                for (int t = 0; t < w.nw; ++t) {
+                for (int t = w.t0; t < w.t0 + w.nw; ++t) {
                     if (!(ok = free(bar_qe, qn, L::QS))) break;
                     const int row = (w.b * a.Hq + w.g * a.rep + t / w.tiles) * a.Lq + w.base + (t % w.tiles) * 128;
                     const uint32_t q = sb + L::kOffQ + (qn % L::QS) * 2 * L::kTile, bq = bar_qf + 8 * (qn % L::QS);
@@ -554,7 +596,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const uint32_t kt = sb + (kn % L::KS) * 2 * L::kTile;
             if (!(ok = wait(bar_kf + 8 * (kn % L::KS), kn / L::KS))) break;
             // half within the tile and step within the head, for the scores and for the products
-            int sh = 0, sk = 0, ph = 0, pk_ = 0;
+            int sh = 0, sk = w.u0 % w.per, ph = 0, pk_ = sk;
             auto scores = [&](int u) {
                 const int s = sw % L::QS, buf = sn & 1;
                 if (sn >= 2 && !wait(bar_ee + 8 * buf, (sn >> 1) - 1)) return false;  // the buffer's last planes are used
@@ -627,67 +669,31 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         __syncwarp();
         wait_bar(bar_dr, 0, lim.drain_ns, nullptr);
     } else if (warp == kSoftWarps + 2) {
-        // ------------------------------------------------------------ the items' exponents and the queries' vectors
+        // ------------------------------------------------------------ the queries' vectors
         bool ok = true;
-        int xn = 0, ln = 0, cn = 0;  // items of few, of many queries; steps
-        for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        int cn = 0;  // steps
+        for (int item = blockIdx.x; item < items && ok; item += gridDim.x) {
             const KeyItem w = key_item(a, item);
+            if (w.nu == 0) continue;
             const int64_t row0 = ((int64_t)w.b * a.Hq + w.g * a.rep) * a.Lq;
-            int pi = 0, c = 0;
-            if (is_long(w)) {
-                long_exponents(w, ln & 1, -1, pi, c);  // (the softmax warps meet here after a failure too)
-                ++ln;
-                if (!ok) continue;
-            } else {
-                if (!ok) continue;
-                const int total = w.n * a.rep;
-                int m = INT_MAX;
-#pragma unroll 4
-                for (int t = lane; t < total; t += 32) {
-                    const int S = a.stats[row_of(w, t)].y;
-                    m = S > 0 ? min(m, S) : m;
-                }
-                m = -warp_max(-m);
-                pi = m == INT_MAX ? 0 : 31 - __clz(m);
-                if (MODE & 2) {
-                    unsigned long long x = 0;
-#pragma unroll 4
-                    for (int t = lane; t < total; t += 32) {
-                        const int64_t at = row_of(w, t);
-                        const int S = a.stats[at].y;
-                        if (S > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), a.tmax[at], a.row[at].y));
-                    }
-                    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-                    c = max(0, 64 - __clzll((long long)x) - 14);
-                }
-                const int xs = xn & 1;
-                if (xn >= 2) ok = __all_sync(0xffffffffu, wait_bar(bar_xe + 8 * xs, ((xn >> 1) - 1) & 1, lim.wait_ns, abort_flag));
-                if (!ok) {
-                    if (lane == 0) fail();
-                    continue;
-                }
-                if (lane == 0) {
-                    misc[4 + 2 * xs] = pi;
-                    misc[5 + 2 * xs] = c;
-                    mbar_arrive(bar_xf + 8 * xs);
-                }
-                ++xn;
-            }
+            const int2 ex = a.exps[w.slot];
+            const int pi = ex.x;
+            const float2 fs = make_float2(attn_factor(a, w.bg), pow2f(-ex.y));
             // two queries per lane and step, read one step ahead
             int2 st[2], rw[2];
             auto fetch = [&](int u) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const int i = w.base + (u % w.per) * kStep + 2 * lane + k;
+                    const int i = w.base + ((w.u0 + u) % w.per) * kStep + 2 * lane + k;
                     st[k] = rw[k] = make_int2(0, 0);
                     if (u < w.nu && i < w.nq) {
-                        const int64_t at = row0 + (int64_t)(u / w.per) * a.Lq + i;
+                        const int64_t at = row0 + (int64_t)((w.u0 + u) / w.per) * a.Lq + i;
                         st[k] = a.stats[at];
                         if (MODE & 2) rw[k] = a.row[at];
                     }
                 }
             };
-            if (w.nu > 0) fetch(0);
+            fetch(0);
             for (int u = 0; u < w.nu && ok; ++u) {
                 float mm[2], r[2], d[2];
 #pragma unroll
@@ -700,10 +706,11 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 fetch(u + 1);
                 const int s = cn & 3;
                 if (cn >= 4) ok = __all_sync(0xffffffffu, wait_bar(bar_ce + 8 * s, ((cn >> 2) - 1) & 1, lim.wait_ns, abort_flag));
-                float *v = (float *)(smem + L::kOffVec) + s * 3 * kStep + 2 * lane;
+                float *v = (float *)(smem + L::kOffVec) + s * L::kVec + 2 * lane;
                 *reinterpret_cast<float2 *>(v) = make_float2(mm[0], mm[1]);
                 *reinterpret_cast<float2 *>(v + kStep) = make_float2(r[0], r[1]);
                 *reinterpret_cast<float2 *>(v + 2 * kStep) = make_float2(d[0], d[1]);
+                if (lane == 0) *reinterpret_cast<float2 *>(v + 3 * kStep) = fs;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar_cf + 8 * s);
                 ++cn;
@@ -718,33 +725,24 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
         const int wg = warp >> 2, et = threadIdx.x & 127, pair = wg >> 1, c0 = (wg & 1) * 32;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
-        int on = 0, xn = 0, ln = 0, cn = 0;  // outputs, items of few and of many queries, steps of the items so far
+        int on = 0, cn = 0;  // outputs, steps of the items so far
         for (int item = blockIdx.x; item < items; item += gridDim.x) {  // (outputs are written after a failure too)
             const KeyItem w = key_item(a, item);
+            if (w.join == 0) continue;
             const int j = w.j0 + et;
-            int pi, cexp;
-            if (is_long(w)) {
-                long_exponents(w, ln & 1, (int)threadIdx.x, pi, cexp);
-                ++ln;
-            } else {
-                const int xs = xn & 1;
-                ok = ok && __all_sync(0xffffffffu, wait_bar(bar_xf + 8 * xs, (xn >> 1) & 1, lim.wait_ns, abort_flag));
-                pi = misc[4 + 2 * xs], cexp = misc[5 + 2 * xs];
-                warp_arrive(bar_xe + 8 * xs);
-                ++xn;
-            }
-            const f2 f = pk(attn_factor(a, w.bg)), sc = pk(pow2f(-cexp));
             const int lo_i = a.causal ? j - w.off : 0;  // the first query that sees this key
             const int lo_max = warp_max(lo_i);
             const int u0 = (pair ^ cn) & 1;
-            int k_in = w.per > 0 ? u0 % w.per : 0;
+            int k_in = w.per > 0 ? (w.u0 + u0) % w.per : 0;
             for (int u = u0; u < w.nu && ok; u += 2) {
                 const int cs = (cn + u) & 3, buf = (cn + u) & 1;
                 ok = __all_sync(0xffffffffu, wait_bar(bar_sf + 8 * buf, ((cn + u) >> 1) & 1, lim.wait_ns, abort_flag) &&
                                                  wait_bar(bar_cf + 8 * cs, ((cn + u) >> 2) & 1, lim.wait_ns, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                const float *vec = (const float *)(smem + L::kOffVec) + cs * 3 * kStep + c0;
+                const float *vec = (const float *)(smem + L::kOffVec) + cs * L::kVec + c0;
+                const float2 fs = *reinterpret_cast<const float2 *>(vec - c0 + 3 * kStep);
+                const f2 f = pk(fs.x), sc = pk(fs.y);
                 const int i = w.base + k_in * kStep + c0;
                 const uint32_t mine = tm + lanes + buf * 128 + c0;
 #pragma unroll 1
@@ -784,6 +782,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const int turn = on & 1;  // the item's outputs are this turn's pair's; the other goes on
             ++on;
             if (pair != turn) continue;
+            const int2 ex = a.exps[w.slot];  // pi, c
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of + 8 * turn, ((on - 1) >> 1) & 1, lim.wait_ns, abort_flag));
             tc_fence_after();
             const int ed = attn_top(a, OPD, w.bg), ev = attn_top(a, OPV, w.bg), eq = attn_top(a, OPQ, w.bg);
@@ -792,9 +791,21 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const int cc = MODE == 3 ? 0 : (wg & 1) * 64, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
             float2 *gm = (float2 *)(smem + L::kOffRed) + (turn * 2 + (MODE == 3 ? wg & 1 : 0)) * 4 * 128 + et;
             const int den = ok && j < w.nk ? 1 : 0;
+            const AccCols sums{tm + lanes + acc, DP, ok};
+            if (w.join > 1) {
+                // [block][256 columns][128 keys]; heads of 128: dV's after dK's
+                const int64_t at = (MODE == 1 ? a.blocks : 0) + w.slot;
+                int32_t *row_sums = a.join + (at * 256 + (MODE == 3 ? (wg & 1) * 128 : cc)) * 128 + et;
+                const bool last = join_parts(sums, cc, row_sums, DP, (threadIdx.x & 255) == 0 ? a.tickets + at : nullptr, w.join,
+                                             misc + 2 + turn, 1 + turn, NS / 2);
+                if (!last) {
+                    warp_arrive(bar_oe);
+                    continue;
+                }
+            }
             fit_row_tmem<4>(a, is_k ? a.dk : a.dv, row, w.g, cc, den, is_k ? a.mul : 1,
-                            is_k ? cexp - pi - a.shift + ed + ev + eq : ed - pi, live, (int64_t)w.nq * a.rep <= 1024, gm, 128,
-                            MODE == 3 ? 6 + wg : 1 + turn, MODE == 3 ? 128 : NS / 2, AccCols{tm + lanes + acc, DP, ok});
+                            is_k ? ex.y - ex.x - a.shift + ed + ev + eq : ed - ex.x, live, (int64_t)w.nq * a.rep <= 1024, gm, 128,
+                            MODE == 3 ? 6 + wg : 1 + turn, MODE == 3 ? 128 : NS / 2, sums);
             warp_arrive(bar_oe);
         }
         if (!ok && lane == 0) fail();

@@ -267,6 +267,25 @@ def test_extreme_lengths(ict, case):
     status_ok(ict)
 
 
+@pytest.mark.parametrize("lens_q,lens_k,causal,D", [
+    ([140, 3, 0, 129], [150, 150, 150, 0], False, 64), ([140, 70, 1, 129], [150, 20, 129, 64], True, 64),
+    ([140, 3, 0, 129], [150, 150, 150, 0], True, 128), ([140, 70, 1, 129], [150, 20, 129, 64], False, 112)])
+def test_few_key_blocks(ict, lens_q, lens_k, causal, D):
+    """Key blocks whose queries (eight heads of up to two tiles each) are shared by several thread blocks."""
+    Case(D + causal, 4, 8, 1, 140, 150, D, causal, lens_q, lens_k, G=16).check(ict, 16)
+    status_ok(ict)
+
+
+@pytest.mark.parametrize("case", [
+    dict(op="attn_bwd", B=2, Hq=6, Hkv=2, Lq=700, Lk=520, D=128, causal=True, ragged=True, packed=False, G=64),
+    dict(op="attn_bwd", B=1, Hq=1, Hkv=1, Lq=3000, Lk=3000, D=64, causal=True, ragged=False, packed=True, G=32),
+    dict(op="attn_bwd", B=1, Hq=4, Hkv=4, Lq=2500, Lk=130, D=80, causal=False, ragged=False, packed=False, G=80),
+])
+def test_few_long_key_blocks(ict, case):
+    _compare(_operators(), case, 4)
+    status_ok(ict)
+
+
 def test_streams_and_graph(ict):
     """The same calls on two streams at once and as one replayed graph: a transformer layer's norm, attention and
     both backward passes, each with its own workspace."""
