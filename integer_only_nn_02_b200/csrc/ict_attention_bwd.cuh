@@ -348,8 +348,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             float2 *gm = (float2 *)(smem + L::kOffRed) + turn * 8 * 128 + et;
             fit_row_tmem<DP / 32>(a, a.o, (int64_t)w.b * a.Lq + i, w.h, (wg & 1) * (DP / 2), ok ? st.y : 0, a.mul,
                                   tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
-                                  w.nk <= 1024, gm, 128, 1 + turn, NS / 2, AccCols{tm + lanes + L::kAcc, DP, ok});
-            warp_arrive(bar_oe);
+                                  w.nk <= 1024, gm, 128, 1 + turn, NS / 2, AccCols{tm + lanes + L::kAcc, DP, ok}, bar_oe);
             ++on;
         }
         if (!ok && lane == 0) fail();
@@ -640,9 +639,11 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 const uint64_t dq = smem_desc_mnmajor64(q, kHalfTile), dd = smem_desc_mnmajor64(q + L::kTile, kHalfTile);
                 const uint32_t e0 = tm + buf * 128, first = u ? 1u : 0u;
                 const bool done = pk_ + 1 == w.per || ph == 1;
+                const int ks = (min(kStep, w.nq - w.base - pk_ * kStep) + 31) / 32;
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2; ++kk) {
+                        if (kk >= ks) break;
                         if (MODE & 1) {
                             umma_i8_ta(tm + kAccCol, e0 + kk * 32, dd + 128 * kk, kIdHi, kk ? 1u : first);
                             umma_i8_ta(tm + kAccCol + DP, e0 + kk * 32 + 8, dd + 128 * kk, kIdLo, kk ? 1u : first);
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 const int i = w.base + k_in * kStep + c0;
                 const uint32_t mine = tm + lanes + buf * 128 + c0;
 #pragma unroll 1
-                for (int c = 0; c < 32; c += 16) {
+                for (int c = 0; c < 32 && i < w.nq; c += 16) {  // (the MMAs read no 32 columns behind the last query)
                     uint32_t vs[16], vd[16], plo[4], phi[4], ulo[4], uhi[4];
                     tmem_ld16(mine + c, vs);
                     if (MODE & 2) tmem_ld16(mine + kStep + c, vd);
@@ -805,8 +806,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             }
             fit_row_tmem<4>(a, is_k ? a.dk : a.dv, row, w.g, cc, den, is_k ? a.mul : 1,
                             is_k ? ex.y - ex.x - a.shift + ed + ev + eq : ed - ex.x, live, (int64_t)w.nq * a.rep <= 1024, gm, 128,
-                            MODE == 3 ? 6 + wg : 1 + turn, MODE == 3 ? 128 : NS / 2, sums);
-            warp_arrive(bar_oe);
+                            MODE == 3 ? 6 + wg : 1 + turn, MODE == 3 ? 128 : NS / 2, sums, bar_oe);
         }
         if (!ok && lane == 0) fail();
     }

@@ -116,7 +116,8 @@ __device__ __forceinline__ GroupFit group_fit(const AccCols &acc, int first, int
     GroupFit f;
     f.e = none ? kEZero : finalize_exp(need + r);
     f.sc = none ? 0.0f : rd * pow2f(min(max(r - f.e, -126), 100));
-    f.lim = fmaf(w * f.sc, -9.5367431640625e-07f, 0.4999999f);  // w sc 2^-20
+    // w sc 2^-20; nothing was rounded (ties included) where den is 1 and every value below 2^24
+    f.lim = den == 1 && w < 16777216.0f ? 1.0f : fmaf(w * f.sc, -9.5367431640625e-07f, 0.4999999f);
     return f;
 }
 
@@ -156,52 +157,120 @@ __device__ __forceinline__ void round16(const AccCols &acc, int col, const float
     if (live) *reinterpret_cast<uint4 *>(dst) = make_uint4(w0, w1, w2, w3);
 }
 
+// What fp32 cannot decide, out of line: the exponent of the largest magnitude; 16 mantissas of which
+// some lie too close to a border.
+__device__ __noinline__ int exact_need(int m, int mul, int den) { return need_quot((double)m * (double)mul / (double)den); }
+__device__ __noinline__ uint4 exact_round16(const int *x, uint4 w, int e, float sc, float lim, int r, int mul, int den) {
+    uint32_t near = e == 127 ? 0xffff : 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+        const float n = (float)x[q], k = fmaf(n, sc, kAttnMagic);
+        if (!(fabsf(fmaf(n, sc, kAttnMagic - k)) < lim)) near |= 1u << q;
+    }
+    const double rden = pow2d(r - e) * (double)mul / (double)den;
+#pragma unroll 1
+    for (; near; near &= near - 1) {
+        const int q = __ffs(near) - 1, k = q >> 2;
+        const int y = e == 127 ? (int)fmin(fmax(x[q] * rden, -127.0), 127.0) : quot_mant_fast(x[q], rden);
+        const uint32_t sh = 8 * (q & 3), keep = ~(0xffu << sh), put = (uint32_t)(y & 0xff) << sh;
+        w.x = k == 0 ? (w.x & keep) | put : w.x;
+        w.y = k == 1 ? (w.y & keep) | put : w.y;
+        w.z = k == 2 ? (w.z & keep) | put : w.z;
+        w.w = k == 3 ? (w.w & keep) | put : w.w;
+    }
+    return w;
+}
+
+// FIT of 16 SEGS columns in groups of one or two segments: 32 columns at a time stay in registers
+// between the maximum and the rounding, and the accumulators are free for the next item once the
+// last of them are read.
+template <int SEGS>
+__device__ __forceinline__ void fit_row_regs(const AttnArgs &a, int8_t *dst, int8_t *oe, int c0, int gs, int den, int mul,
+                                             int r, bool live, bool some, float rd, const AccCols &acc, uint32_t release) {
+    const f2 M = pk(kAttnMagic);
+#pragma unroll 1
+    for (int h = 0; h < SEGS; h += 2) {
+        const int c = c0 + 16 * h;
+        int x[32], m[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            uint32_t hi[16], lo[16];
+            acc.load16(c + 16 * s, hi, lo);
+            int top = 0, low = 0;
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+                x[16 * s + q] = (int)hi[q] * 256 + (int)lo[q];
+                x[16 * s + q + 1] = (int)hi[q + 1] * 256 + (int)lo[q + 1];
+                top = __vimax3_s32(top, x[16 * s + q], x[16 * s + q + 1]);
+                low = __vimin3_s32(low, x[16 * s + q], x[16 * s + q + 1]);
+            }
+            m[s] = max(top, -low);
+        }
+        if (release && h + 2 >= SEGS) warp_arrive(release);
+        int e = kEZero;
+        float sc = 0.0f, lim = 0.5f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            if (c + 16 * s >= a.D) break;
+            if (s == 0 || gs == 1) {
+                const int mi = gs == 1 ? m[s] : max(m[0], m[1]);
+                // four roundings: the magnitude, the divisor, the factor, the product
+                const float w = (float)mi, q0 = w * rd, dq = q0 * 4.76837158203125e-07f;  // 2^-21
+                const bool zero = !some || mi == 0;
+                const int n0 = zero ? 0 : need_rel_f32(__float_as_uint(fmaxf(q0 - dq, 1.17549435e-38f)), 8);
+                int need = zero ? 0 : need_rel_f32(__float_as_uint(q0 + dq), 8);
+                if (n0 != need) need = exact_need(mi, mul, den);
+                e = zero ? kEZero : finalize_exp(need + r);
+                sc = zero ? 0.0f : rd * pow2f(min(max(r - e, -126), 100));
+                // three roundings: w sc 2^-22; none at all (ties included) where den is 1 and every value below 2^24
+                lim = den == 1 && mi < (1 << 24) ? 1.0f : fmaf(w * sc, -2.38418579e-07f, 0.4999999f);
+                if (live) oe[(c + 16 * s) / (16 * gs)] = (int8_t)e;
+            }
+            const f2 scp = pk(sc);
+            uint32_t v[16];
+            float far = 0;  // from a whole number
+#pragma unroll
+            for (int q = 0; q < 16; q += 2) {
+                const f2 n = pk((float)x[16 * s + q], (float)x[16 * s + q + 1]), w = fma2(n, scp, M);
+                float w0, w1, d0, d1;
+                unpk(w, w0, w1);
+                unpk(fma2(n, scp, sub2(M, w)), d0, d1);  // what the rounding took away
+                far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
+                v[q] = __float_as_uint(w0), v[q + 1] = __float_as_uint(w1);
+            }
+            uint4 w = make_uint4(pack4b(v[0], v[1], v[2], v[3]), pack4b(v[4], v[5], v[6], v[7]),
+                                 pack4b(v[8], v[9], v[10], v[11]), pack4b(v[12], v[13], v[14], v[15]));
+            if (!(far < lim) || e == 127) {
+                int y[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) y[q] = x[16 * s + q];
+                w = exact_round16(y, w, e, sc, lim, r, mul, den);
+            }
+            if (live) *reinterpret_cast<uint4 *>(dst + c + 16 * s) = w;
+        }
+    }
+}
+
 // FIT of one row's accumulators (this thread's TMEM lane): quotients (256 hi + lo) mul / den at
-// exponent r, SEGS segments of 16 columns from column c0 of head h.
+// exponent r, SEGS segments of 16 columns from column c0 of head h; then they are released.
 // Magnitudes and mantissas are computed in fp32 with an error bound; what lies within the bound
-// of a border between two results (a mantissa in some ten thousand) is read again and decided
-// in fp64, where the quotient's rounding to 53 bits cannot hide the border.  narrow: the
-// accumulators 256 hi + lo fit 32 bits.  Groups of 32 columns inside this thread's columns stay
-// in registers between the maximum and the rounding; for other groups the threads that share
-// the row join their segments' maxima in gmax (shared memory, [segment][stride]) and read the
-// accumulators twice.
+// of a border between two results (a mantissa in some ten thousand) is decided in fp64, where
+// the quotient's rounding to 53 bits cannot hide the border.  narrow: the accumulators
+// 256 hi + lo fit 32 bits; groups of 16 and 32 columns then stay in registers.  For other
+// groups the threads that share the row join their segments' maxima in gmax (shared memory,
+// [segment][stride]) and read the accumulators twice.
 template <int SEGS>
 __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &out, int64_t row, int h, int c0, int den,
                                              int mul, int r, bool live, bool narrow, float2 *gmax, int stride, int bar,
-                                             int nthreads, const AccCols &acc) {
+                                             int nthreads, const AccCols &acc, uint32_t release) {
     const int col = out.col + h * a.D;
     const int gs = out.G / 16;  // segments of a group
     const bool some = live && den != 0;
     // relative error below 2^-22 (two roundings); a quotient's, accumulator included, below err 2^-21
     const float rd = some ? __fdiv_rn((float)mul, (float)den) : 0.0f;
     int8_t *dst = out.mant + row * out.ld + col, *oe = out.exp + row * out.ngc + col / out.G;
-    if (SEGS % 2 == 0 && gs == 2 && narrow) {
-#pragma unroll 1
-        for (int s = 0; s < SEGS; s += 2) {
-            const int c = c0 + 16 * s;
-            if (c >= a.D) break;
-            float n0[16], n1[16];
-            uint32_t hi[16], lo[16];
-            int mi = 0;
-            acc.load16(c, hi, lo);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int x = (int)hi[q] * 256 + (int)lo[q];
-                mi = max(mi, abs(x));
-                n0[q] = (float)x;
-            }
-            acc.load16(c + 16, hi, lo);
-#pragma unroll
-            for (int q = 0; q < 16; ++q) {
-                const int x = (int)hi[q] * 256 + (int)lo[q];
-                mi = max(mi, abs(x));
-                n1[q] = (float)x;
-            }
-            const GroupFit f = group_fit(acc, c, 32, (float)mi, (float)mi, some, rd, den, mul, r);
-            if (live) oe[c / 32] = (int8_t)f.e;
-            round16(acc, c, n0, f, some, den, mul, r, live, dst + c);
-            round16(acc, c + 16, n1, f, some, den, mul, r, live, dst + c + 16);
-        }
+    if (SEGS % 2 == 0 && gs <= 2 && narrow) {
+        fit_row_regs<SEGS>(a, dst, oe, c0, gs, den, mul, r, live, some, rd, acc, release);
         return;
     }
 #pragma unroll 1
@@ -244,6 +313,7 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
         }
         round16(acc, seg * 16, n, f, some, den, mul, r, live, dst + seg * 16);
     }
+    if (release) warp_arrive(release);
 }
 
 // 32 scores of a row to the two byte planes of their weights; PART: only the first `vis`
@@ -582,11 +652,9 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             float2 *gm = (float2 *)(smem + L::kOffRed + 2048) + et;
             fit_row_tmem<DP / NWG / 16>(
                 a, a.o, (int64_t)w.b * a.Lq + i, w.h, c0, read ? (int)sum : 0, 1, attn_top(a, OPV, w.b * a.Hkv + w.g), live,
-                w.nk <= 1024, gm, 128, 1, NS, AccCols{tm + lanes + L::kO, DP, read});
-            if (w.nt > 0) {
-                warp_arrive(bar_oe);
-                ++on;
-            }
+                w.nk <= 1024, gm, 128, 1, NS, AccCols{tm + lanes + L::kO, DP, read},
+                w.nt > 0 ? bar_oe : 0);
+            if (w.nt > 0) ++on;
         }
         if (!ok && lane == 0) fail();
     }
