@@ -272,7 +272,7 @@ Scratch scratch(const AttnArgs &a, bool back) {
     s.copy[OPD] = take(back ? q * a.Dp : 0);
     s.row = take(back ? q * 8 : 0);
     s.tmax = take(back ? q * 4 : 0);
-    s.exps = take(back ? (int64_t)a.blocks * 8 : 0);
+    s.exps = take(back ? (int64_t)a.blocks * 16 : 0);
     if (back && a.parts > 1) {
         const int64_t n = (int64_t)a.blocks * (a.Dp / 64);
         s.tickets = take(n * 4);
@@ -510,7 +510,7 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     output(a.dv, dV, d->v_col);
     a.row = (int2 *)(base + w.row);
     a.tmax = (int32_t *)(base + w.tmax);
-    a.exps = (int2 *)(base + w.exps);
+    a.exps = (int4 *)(base + w.exps);
     if (a.parts > 1) a.tickets = (int32_t *)(base + w.tickets), a.join = (int32_t *)(base + w.join);
     if (rq == 0 && rk == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;

@@ -44,7 +44,7 @@ struct AttnArgs {
     int2 *row;           // [B * Hq * Lq]: delta', X
     int32_t *tmax;       // [B * Hq * Lq]: largest |T| of the row
     AttnOut dk, dv;
-    int2 *exps;          // [key blocks * B * Hkv]: pi, c
+    int4 *exps;          // [key blocks * B * Hkv]: pi, c, exponents of the sums of dV and dK
     int parts, blocks;   // each key block's queries are shared by so many; key blocks * B * Hkv
     int32_t *join, *tickets;  // with parts > 1: their sums, and how many have added theirs
 };

@@ -372,9 +372,9 @@ struct DkvCfg {
     static constexpr int kOffQ = KS * 2 * kTile;                           // K stage: K tile, V tile; Q stage: Q tile, dO tile
     static constexpr int kVec = 3 * kStep + 4;                             // a step's floats: see dkv16, then f and 2^-c
     static constexpr int kOffVec = kOffQ + QS * 2 * kTile;                 // [4][kVec] floats
-    static constexpr int kOffRed = kOffVec + 4 * kVec * 4;                 // [4][4][128] float2
-    static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8;
-    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 6;
+    static constexpr int kOffRed = kOffVec + 4 * kVec * 4;                 // [8][128] float2
+    static constexpr int kOffBar = kOffRed + 8 * 128 * 8;
+    static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 5;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 96;
 };
@@ -416,7 +416,7 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
 }
 
 // The exponents of every key block: pi from the smallest sum of weights, c from the largest bound,
-// over the queries that see the block.  One block of threads each, of up to 1024.
+// over the queries that see the block; those of the accumulators of dV and dK.  One block of threads each, of up to 1024.
 __global__ void __launch_bounds__(1024) attn_exps_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ int smin;
     __shared__ unsigned long long bmax;
@@ -451,16 +451,20 @@ __global__ void __launch_bounds__(1024) attn_exps_kernel(const __grid_constant__
     for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
     if ((threadIdx.x & 31) == 0) atomicMax(&bmax, x);
     __syncthreads();
-    if (threadIdx.x == 0) a.exps[blockIdx.x] = make_int2(pi, max(0, 64 - __clzll((long long)bmax) - 14));
+    if (threadIdx.x == 0) {
+        const int c = max(0, 64 - __clzll((long long)bmax) - 14);
+        const int ed = attn_top(a, OPD, bg), ev = attn_top(a, OPV, bg), eq = attn_top(a, OPQ, bg);
+        a.exps[blockIdx.x] = make_int4(pi, c, ed - pi, c - pi - a.shift + ed + ev + eq);
+    }
 }
 
 // A part's sums join the other parts' in memory: 32-bit integers, so that their order does not
 // matter.  The last part to come (true) takes the totals back into its accumulators.  sums: this
-// thread's row of [columns][128 keys] (high planes' 64 columns; low planes lo_cols further on).
+// thread's row of [columns][128 keys] (32 of the high plane, those of the low plane lo_cols further on).
 __device__ __noinline__ bool join_parts(const AccCols acc, int c0, int32_t *sums, int lo_cols, int *tickets, int join,
                                         volatile int *shared, int bar, int nthreads) {
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 16) {
+    for (int c = 0; c < 32; c += 16) {
         uint32_t hi[16], lo[16];
         acc.load16(c0 + c, hi, lo);
 #pragma unroll
@@ -476,7 +480,7 @@ __device__ __noinline__ bool join_parts(const AccCols acc, int c0, int32_t *sums
     if (*shared != join - 1) return false;
     __threadfence();
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 4) {
+    for (int c = 0; c < 32; c += 4) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -506,8 +510,8 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
     const uint32_t bar_qf = bar_ke + 8 * L::KS, bar_qe = bar_qf + 8 * L::QS;
     const uint32_t bar_sf = bar_qe + 8 * L::QS, bar_ef = bar_sf + 16;
     const uint32_t bar_cf = bar_ef + 16, bar_ce = bar_cf + 32;  // the queries' vectors full / empty
-    const uint32_t bar_ee = bar_ce + 32, bar_of = bar_ee + 16, bar_oe = bar_of + 16, bar_dr = bar_oe + 8;
-    volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);  // tmem, abort, a ticket per pair
+    const uint32_t bar_ee = bar_ce + 32, bar_of = bar_ee + 16, bar_oe = bar_of + 8, bar_dr = bar_oe + 8;
+    volatile int *misc = (volatile int *)(smem + L::kOffBar + L::kBars * 8);  // tmem, abort, ticket
     volatile int *abort_flag = &misc[1];
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == NS) {
@@ -523,8 +527,8 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             mbar_init(bar_ee + 8 * s, 1);
         }
         for (int s = 0; s < 4; ++s) mbar_init(bar_cf + 8 * s, 1), mbar_init(bar_ce + 8 * s, kSoftWarps / 2);
-        for (int s = 0; s < 2; ++s) mbar_init(bar_of + 8 * s, 1);  // per pair: each sees every other output
-        mbar_init(bar_oe, kSoftWarps / 2);
+        mbar_init(bar_of, 1);
+        mbar_init(bar_oe, kSoftWarps);
         mbar_init(bar_dr, 1);
         misc[1] = 0;
         fence_barrier_init();
@@ -655,7 +659,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                     }
                     if (done) umma_commit(bar_qe + 8 * s);
                     umma_commit(bar_ee + 8 * buf);
-                    if (u + 1 == w.nu) umma_commit(bar_of + 8 * (on & 1));
+                    if (u + 1 == w.nu) umma_commit(bar_of);
                 }
                 __syncwarp();
                 ++pn;
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const KeyItem w = key_item(a, item);
             if (w.nu == 0) continue;
             const int64_t row0 = ((int64_t)w.b * a.Hq + w.g * a.rep) * a.Lq;
-            const int2 ex = a.exps[w.slot];
+            const int4 ex = a.exps[w.slot];
             const int pi = ex.x;
             const float2 fs = make_float2(attn_factor(a, w.bg), pow2f(-ex.y));
             // two queries per lane and step, read one step ahead
@@ -780,33 +784,27 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 }
                 continue;
             }
-            const int turn = on & 1;  // the item's outputs are this turn's pair's; the other goes on
+            // 32 columns of one gradient per warpgroup
+            const bool is_k = MODE == 3 ? wg >= 2 : MODE == 2;
+            const int cc = MODE == 3 ? (wg & 1) * 32 : wg * 32, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
+            const int4 ex = a.exps[w.slot];
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
             ++on;
-            if (pair != turn) continue;
-            const int2 ex = a.exps[w.slot];  // pi, c
-            if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of + 8 * turn, ((on - 1) >> 1) & 1, lim.wait_ns, abort_flag));
             tc_fence_after();
-            const int ed = attn_top(a, OPD, w.bg), ev = attn_top(a, OPV, w.bg), eq = attn_top(a, OPQ, w.bg);
-            // 64 columns of one gradient per warpgroup
-            const bool is_k = MODE == 3 ? (wg & 1) == 1 : MODE == 2;
-            const int cc = MODE == 3 ? 0 : (wg & 1) * 64, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
-            float2 *gm = (float2 *)(smem + L::kOffRed) + (turn * 2 + (MODE == 3 ? wg & 1 : 0)) * 4 * 128 + et;
-            const int den = ok && j < w.nk ? 1 : 0;
             const AccCols sums{tm + lanes + acc, DP, ok};
             if (w.join > 1) {
                 // [block][256 columns][128 keys]; heads of 128: dV's after dK's
                 const int64_t at = (MODE == 1 ? a.blocks : 0) + w.slot;
-                int32_t *row_sums = a.join + (at * 256 + (MODE == 3 ? (wg & 1) * 128 : cc)) * 128 + et;
-                const bool last = join_parts(sums, cc, row_sums, DP, (threadIdx.x & 255) == 0 ? a.tickets + at : nullptr, w.join,
-                                             misc + 2 + turn, 1 + turn, NS / 2);
-                if (!last) {
+                int32_t *row_sums = a.join + (at * 256 + (MODE == 3 && is_k ? 128 : 0) + cc) * 128 + et;
+                if (!join_parts(sums, cc, row_sums, DP, threadIdx.x == 0 ? a.tickets + at : nullptr, w.join, misc + 2, 1, NS)) {
                     warp_arrive(bar_oe);
                     continue;
                 }
             }
-            fit_row_tmem<4>(a, is_k ? a.dk : a.dv, row, w.g, cc, den, is_k ? a.mul : 1,
-                            is_k ? ex.y - ex.x - a.shift + ed + ev + eq : ed - ex.x, live, (int64_t)w.nq * a.rep <= 1024, gm, 128,
-                            MODE == 3 ? 6 + wg : 1 + turn, MODE == 3 ? 128 : NS / 2, sums, bar_oe);
+            float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 4 * 128 : 0) + et;
+            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, row, w.g, cc, ok && j < w.nk ? 1 : 0, is_k ? a.mul : 1, is_k ? ex.w : ex.z, live,
+                            (int64_t)w.nq * a.rep <= 1024, gm, 128, MODE == 3 ? 2 + (wg >> 1) : 1, MODE == 3 ? NS / 2 : NS, sums,
+                            bar_oe);
         }
         if (!ok && lane == 0) fail();
     }
