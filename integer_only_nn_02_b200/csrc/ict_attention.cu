@@ -212,6 +212,12 @@ int split_parts(const AttnArgs &a) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(kSplitTarget / a.blocks, tiles / kSplitTiles));
 }
 
+Div divide_by(int d) {  // d >= 1
+    int l = 0;
+    while ((1u << l) < (unsigned)d) ++l;
+    return Div{(uint32_t)(((1ull << 32) * ((1ull << l) - (unsigned)d)) / (unsigned)d + 1), l};
+}
+
 int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
     if (!d) return ICT_ERR_INVALID_ARG;
     if (d->batch < 0 || d->heads_q < 1 || d->heads_kv < 1 || d->len_q < 0 || d->len_k < 0 || d->head_dim < 1 ||
@@ -231,6 +237,8 @@ int plan(AttnArgs &a, const ict_attn_desc *d, bool back) {
     a.n_op = back ? 4 : 3;
     a.blocks = (int)(host::cdiv(a.Lk, kKeyBlock) * a.B * a.Hkv);
     a.parts = back ? split_parts(a) : 1;
+    a.heads_q = divide_by(std::max(1, a.B * a.Hq)), a.hq = divide_by(a.Hq), a.by_rep = divide_by(a.rep);
+    a.heads_kv = divide_by(std::max(1, a.B * a.Hkv)), a.hkv = divide_by(a.Hkv);
     return ICT_OK;
 }
 
@@ -287,9 +295,10 @@ void operand(AttnOperand &o, const ict_tensor *t, int col, int heads, int L, con
     o.gsh = (o.gv & (o.gv - 1)) == 0 ? __builtin_ctz((unsigned)o.gv) : -1;
     o.col = col, o.heads = heads, o.L = L, o.lens = lens, o.copy = copy;
 }
-void output(AttnOut &o, const ict_tensor *t, int col) {
+void output(AttnOut &o, const ict_tensor *t, int col, int D) {
     o.mant = t->mant, o.exp = t->exp, o.ld = t->ld, o.ngc = groups_per_row(t);
     o.G = (int)std::min<int64_t>(t->g_cols, t->cols), o.col = col;
+    o.gcol = col / o.G, o.dg = D / o.G;
 }
 
 // Common to both directions: checks, workspace, operands.
@@ -477,7 +486,7 @@ int32_t ict_attention_fwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     if ((st = setup(a, w, d, false, Q, K, V, lens_q, lens_k, stats, ws, ws_bytes))) return st;
     if ((st = check_out(O, (int64_t)a.B * a.Lq, 0, (int64_t)a.Hq * a.D, a.D))) return st;
     if ((st = host::device_info(nullptr))) return st;
-    output(a.o, O, 0);
+    output(a.o, O, 0, a.D);
     const int64_t rows = (int64_t)a.B * a.Hq * a.Lq;
     if (rows == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;
@@ -505,9 +514,9 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     uint8_t *base = (uint8_t *)ws;
     operand(a.op[OPD], dO, 0, a.Hq, a.Lq, lens_q, (int8_t *)(base + w.copy[OPD]));
     a.o_mant = O->mant, a.o_exp = O->exp, a.o_ld = O->ld, a.o_ngc = groups_per_row(O), a.o_gv = vec_per_group(O);
-    output(a.o, dQ, d->q_col);
-    output(a.dk, dK, d->k_col);
-    output(a.dv, dV, d->v_col);
+    output(a.o, dQ, d->q_col, a.D);
+    output(a.dk, dK, d->k_col, a.D);
+    output(a.dv, dV, d->v_col, a.D);
     a.row = (int2 *)(base + w.row);
     a.tmax = (int32_t *)(base + w.tmax);
     a.exps = (int4 *)(base + w.exps);

@@ -22,16 +22,24 @@ struct AttnOperand {
     const int32_t *lens;
     int8_t *copy;     // aligned copy [B][heads][L][Dp]
 };
+// n / d for 0 <= n < 2^31 by a multiplication (a division costs every warp some hundred cycles)
+struct Div {
+    uint32_t m;
+    int s;
+    __device__ __forceinline__ int operator()(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> s); }
+};
 struct AttnOut {
     int8_t *mant, *exp;
     int64_t ld;
     int ngc, G, col;
+    int gcol, dg;        // groups before the first head, groups of a head
 };
 
 struct AttnArgs {
     AttnOperand op[OPN];
     int n_op;
     int B, Hq, Hkv, rep, Lq, Lk, D, Dp, causal;
+    Div heads_q, hq, by_rep, heads_kv, hkv;  // divisions by B Hq, Hq, rep, B Hkv, Hkv
     int mul, shift;
     float fmul;          // rn24(mul * log2(e) * 2^23)
     int32_t *top;        // [n_op][B * Hkv]: exponent of the aligned operand, very negative when all zero

@@ -89,7 +89,7 @@ __device__ __forceinline__ void zero_row(const AttnArgs &a, const AttnOut &out, 
     const int col = out.col + h * a.D, end = min(a.D, c0 + n);
     for (int c = c0; c < end; c += 16) {
         *reinterpret_cast<uint4 *>(out.mant + row * out.ld + col + c) = make_uint4(0, 0, 0, 0);
-        if (c % out.G == 0) out.exp[row * out.ngc + (col + c) / out.G] = (int8_t)kEZero;
+        if (c % out.G == 0) out.exp[row * out.ngc + out.gcol + h * out.dg + c / out.G] = (int8_t)kEZero;
     }
 }
 
@@ -343,12 +343,13 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             }
             named_bar_sync(3 + turn, NS);
             if (wg == 2 * turn && live) a.tmax[at] = max(max(red[et], red[128 + et]), max(red[256 + et], red[384 + et]));
+            const RowOut out = row_out(a, a.o, (int64_t)w.b * a.Lq + i, w.h, st.y, a.mul, live);
+            const int r = tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift;
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of + 8 * turn, (on >> 1) & 1, lim.wait_ns, abort_flag));
             tc_fence_after();
             float2 *gm = (float2 *)(smem + L::kOffRed) + turn * 8 * 128 + et;
-            fit_row_tmem<DP / 32>(a, a.o, (int64_t)w.b * a.Lq + i, w.h, (wg & 1) * (DP / 2), ok ? st.y : 0, a.mul,
-                                  tau + attn_top(a, OPD, bg) + attn_top(a, OPV, bg) + attn_top(a, OPK, bg) - a.shift, live,
-                                  w.nk <= 1024, gm, 128, 1 + turn, NS / 2, AccCols{tm + lanes + L::kAcc, DP, ok}, bar_oe);
+            fit_row_tmem<DP / 32>(a, a.o, out, (wg & 1) * (DP / 2), r, w.nk <= 1024, gm, 128, 1 + turn, NS / 2,
+                                  AccCols{tm + lanes + L::kAcc, DP, ok}, bar_oe);
             ++on;
         }
         if (!ok && lane == 0) fail();
@@ -386,9 +387,10 @@ struct KeyItem {
 };
 __device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
     KeyItem w;
-    const int heads = a.B * a.Hkv, J = item / (heads * a.parts), r = item - J * heads * a.parts, part = r / heads;
-    w.bg = r - part * heads;
-    w.b = w.bg / a.Hkv;
+    const int heads = a.B * a.Hkv, Jp = a.heads_kv(item);  // J parts + part
+    const int J = a.parts == 1 ? Jp : Jp / a.parts, part = Jp - J * a.parts;
+    w.bg = item - Jp * heads;
+    w.b = a.hkv(w.bg);
     w.g = w.bg - w.b * a.Hkv;
     w.j0 = J * kKeyBlock;
     w.slot = J * heads + w.bg;
@@ -402,7 +404,10 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
     w.per = w.n > 0 ? (w.nq - w.base + kStep - 1) / kStep : 0;  // steps of one head
     const int all = w.tiles * a.rep;
     w.join = min(a.parts, max(all, 1));  // parts with work (one for a block that no query sees)
-    w.t0 = w.nw = w.u0 = w.nu = 0;
+    w.t0 = w.u0 = 0;
+    w.nw = all, w.nu = w.per * a.rep;
+    if (a.parts == 1) return w;
+    w.nw = w.nu = 0;
     if (part < w.join && all > 0) {
         const int t1 = all * (part + 1) / w.join;
         w.t0 = all * part / w.join;
@@ -758,7 +763,10 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                     tmem_ld_wait();
                     tmem_tie(vs);
                     if (MODE & 2) tmem_tie(vd);
-                    if (i + c >= lo_max) dkv16<false, MODE>(vs, vd, vec + c, f, sc, 0, plo, phi, ulo, uhi);
+                    if (i + c >= w.nq) {  // no such query
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) plo[q] = phi[q] = ulo[q] = uhi[q] = 0;
+                    } else if (i + c >= lo_max) dkv16<false, MODE>(vs, vd, vec + c, f, sc, 0, plo, phi, ulo, uhi);
                     else dkv16<true, MODE>(vs, vd, vec + c, f, sc, lo_i - i - c, plo, phi, ulo, uhi);
                     if (MODE & 1) {  // in the place of scores already read
                         tmem_st4(mine + c / 4, phi);
@@ -788,6 +796,7 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
             const bool is_k = MODE == 3 ? wg >= 2 : MODE == 2;
             const int cc = MODE == 3 ? (wg & 1) * 32 : wg * 32, acc = MODE == 3 && is_k ? kAccCol + 2 * DP : kAccCol;
             const int4 ex = a.exps[w.slot];
+            const RowOut out = row_out(a, is_k ? a.dk : a.dv, row, w.g, j < w.nk ? 1 : 0, is_k ? a.mul : 1, live);
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
             ++on;
             tc_fence_after();
@@ -802,9 +811,8 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                 }
             }
             float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 4 * 128 : 0) + et;
-            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, row, w.g, cc, ok && j < w.nk ? 1 : 0, is_k ? a.mul : 1, is_k ? ex.w : ex.z, live,
-                            (int64_t)w.nq * a.rep <= 1024, gm, 128, MODE == 3 ? 2 + (wg >> 1) : 1, MODE == 3 ? NS / 2 : NS, sums,
-                            bar_oe);
+            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, out, cc, is_k ? ex.w : ex.z, (int64_t)w.nq * a.rep <= 1024, gm, 128,
+                            MODE == 3 ? 2 + (wg >> 1) : 1, MODE == 3 ? NS / 2 : NS, sums, bar_oe);
         }
         if (!ok && lane == 0) fail();
     }

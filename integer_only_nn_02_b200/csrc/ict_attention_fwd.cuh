@@ -224,7 +224,7 @@ __device__ __forceinline__ void fit_row_regs(const AttnArgs &a, int8_t *dst, int
                 sc = zero ? 0.0f : rd * pow2f(min(max(r - e, -126), 100));
                 // three roundings: w sc 2^-22; none at all (ties included) where den is 1 and every value below 2^24
                 lim = den == 1 && mi < (1 << 24) ? 1.0f : fmaf(w * sc, -2.38418579e-07f, 0.4999999f);
-                if (live) oe[(c + 16 * s) / (16 * gs)] = (int8_t)e;
+                if (live) oe[(c + 16 * s) >> (3 + gs)] = (int8_t)e;  // 16 or 32 columns
             }
             const f2 scp = pk(sc);
             uint32_t v[16];
@@ -259,16 +259,30 @@ __device__ __forceinline__ void fit_row_regs(const AttnArgs &a, int8_t *dst, int
 // 256 hi + lo fit 32 bits; groups of 16 and 32 columns then stay in registers.  For other
 // groups the threads that share the row join their segments' maxima in gmax (shared memory,
 // [segment][stride]) and read the accumulators twice.
-template <int SEGS>
-__device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &out, int64_t row, int h, int c0, int den,
-                                             int mul, int r, bool live, bool narrow, float2 *gmax, int stride, int bar,
-                                             int nthreads, const AccCols &acc, uint32_t release) {
-    const int col = out.col + h * a.D;
-    const int gs = out.G / 16;  // segments of a group
-    const bool some = live && den != 0;
+struct RowOut {  // what is known of a row before its accumulators are complete
+    int8_t *dst, *oe;
+    float rd;
+    int den, mul;
+    bool live, some;
+};
+__device__ __forceinline__ RowOut row_out(const AttnArgs &a, const AttnOut &out, int64_t row, int h, int den, int mul, bool live) {
+    RowOut o;
+    o.dst = out.mant + row * out.ld + out.col + h * a.D;
+    o.oe = out.exp + row * out.ngc + out.gcol + h * out.dg;
+    o.den = den, o.mul = mul, o.live = live, o.some = live && den != 0;
     // relative error below 2^-22 (two roundings); a quotient's, accumulator included, below err 2^-21
-    const float rd = some ? __fdiv_rn((float)mul, (float)den) : 0.0f;
-    int8_t *dst = out.mant + row * out.ld + col, *oe = out.exp + row * out.ngc + col / out.G;
+    o.rd = o.some ? __fdiv_rn((float)mul, (float)den) : 0.0f;
+    return o;
+}
+template <int SEGS>
+__device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &out, const RowOut &o, int c0, int r, bool narrow,
+                                             float2 *gmax, int stride, int bar, int nthreads, const AccCols &acc,
+                                             uint32_t release) {
+    const int gs = out.G / 16;  // segments of a group
+    const float rd = o.rd;
+    const int den = o.den, mul = o.mul;
+    const bool live = o.live, some = o.some;
+    int8_t *dst = o.dst, *oe = o.oe;
     if (SEGS % 2 == 0 && gs <= 2 && narrow) {
         fit_row_regs<SEGS>(a, dst, oe, c0, gs, den, mul, r, live, some, rd, acc, release);
         return;
@@ -344,12 +358,11 @@ struct AttnItem {
 };
 __device__ __forceinline__ AttnItem attn_item(const AttnArgs &a, int item) {
     AttnItem w;
-    const int ntq = (a.Lq + kQTile - 1) / kQTile, heads = a.B * a.Hq;
-    const int tile = ntq - 1 - item / heads;
-    w.bh = item % heads;
-    w.b = w.bh / a.Hq;
+    const int t = a.heads_q(item), tile = (a.Lq + kQTile - 1) / kQTile - 1 - t;
+    w.bh = item - t * a.B * a.Hq;
+    w.b = a.hq(w.bh);
     w.h = w.bh - w.b * a.Hq;
-    w.g = w.h / a.rep;
+    w.g = a.by_rep(w.h);
     w.i0 = tile * kQTile;
     w.nq = clamp_len(a.op[OPQ].lens, w.b, a.Lq);
     w.nk = clamp_len(a.op[OPK].lens, w.b, a.Lk);
@@ -641,19 +654,20 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             red[256 + wg * 128 + et] = (int)sum;
             named_bar_sync(1, NS);
             sum += (uint32_t)red[256 + (wg ^ 1) * 128 + et];
+            const bool live = i < a.Lq;
+            const RowOut row = row_out(a, a.o, (int64_t)w.b * a.Lq + i, w.h, w.nt > 0 ? (int)sum : 0, 1, live);
+            const int top_v = attn_top(a, OPV, w.b * a.Hkv + w.g);
             if (w.nt > 0 && ok) {
                 ok = __all_sync(0xffffffffu, wait_bar(bar_of, on & 1, lim.wait_ns, abort_flag));
                 tc_fence_after();
             }
-            const bool live = i < a.Lq, read = w.nt > 0 && ok;
+            const bool read = w.nt > 0 && ok;
             if (live && wg == 0) a.stats[(int64_t)w.bh * a.Lq + i] = make_int2(mx, (int)sum);
             // outputs: columns [wg DP / NWG, ...) of the head; every thread takes part in the barriers
             const int c0 = wg * (DP / NWG);
             float2 *gm = (float2 *)(smem + L::kOffRed + 2048) + et;
-            fit_row_tmem<DP / NWG / 16>(
-                a, a.o, (int64_t)w.b * a.Lq + i, w.h, c0, read ? (int)sum : 0, 1, attn_top(a, OPV, w.b * a.Hkv + w.g), live,
-                w.nk <= 1024, gm, 128, 1, NS, AccCols{tm + lanes + L::kO, DP, read},
-                w.nt > 0 ? bar_oe : 0);
+            fit_row_tmem<DP / NWG / 16>(a, a.o, row, c0, top_v, w.nk <= 1024, gm, 128, 1, NS,
+                                        AccCols{tm + lanes + L::kO, DP, read}, w.nt > 0 ? bar_oe : 0);
             if (w.nt > 0) ++on;
         }
         if (!ok && lane == 0) fail();
