@@ -111,6 +111,8 @@ __device__ __forceinline__ float row_scale(const NormArgs &p, int s1, int s2, in
     return D > 0 ? __frcp_rn(__fsqrt_rn(__ll2float_rn(D))) : 0.0f;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 template <int L>
 __device__ __forceinline__ int lanes_sum(int v) {
 #pragma unroll
@@ -304,6 +306,13 @@ __global__ void __launch_bounds__(256, V <= 4 ? 3 : (V <= 8 ? 2 : 1)) norm_fwd_k
                 ex[v] = p.x_exp[rr * p.ngx + gi[v]];
             }
         }
+        const int64_t nx = row + (int64_t)gridDim.x * per;
+        if (nx < p.rows) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v * L + lr < p.nvec) prefetch_l2(p.x + nx * p.ldx + (v * L + lr) * 16);
+            if (lr == 0) prefetch_l2(p.x_exp + nx * p.ngx);
+        }
         const int e = align_vectors<L, V>(w, ex, rk);
         int s1 = 0, s2 = 0;
 #pragma unroll
@@ -387,6 +396,17 @@ __global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __g
                 ex[v] = p.x_exp[rr * p.ngx + gi[v]];
                 ed[v] = p.dy_exp[rr * p.ngd + gd[v]];
             }
+        }
+        const int64_t nx = row + (int64_t)gridDim.x * per;
+        if (nx < p.rows) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (v * L + lr < p.nvec) {
+                    prefetch_l2(p.x + nx * p.ldx + (v * L + lr) * 16);
+                    prefetch_l2(p.dy + nx * p.lddy + (v * L + lr) * 16);
+                }
+            if (lr == 0) prefetch_l2(p.x_exp + nx * p.ngx);
+            if (lr == 1) prefetch_l2(p.dy_exp + nx * p.ngd);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v)
