@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ict.h"
 
 namespace ict {
@@ -19,6 +21,18 @@ int check_vec(const ict_tensor *t);  // 16-byte vectors: pointer, ld, cols, grou
 int tmap_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
             uint32_t box_outer, CUtensorMapSwizzle sw);
 void wait_limits(uint64_t *wait_ns, uint64_t *drain_ns);
+
+// Dynamic shared memory of a kernel, set once per device (the call costs a microsecond of every launch).
+template <auto Kernel>
+int allow_smem(int bytes) {
+    static std::atomic<int> set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ICT_ERR_CUDA;
+    if (set[dev].load(std::memory_order_acquire) >= bytes) return ICT_OK;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return ICT_ERR_CUDA;
+    set[dev].store(bytes, std::memory_order_release);
+    return ICT_OK;
+}
 
 // the source files' device status words, OR-ed into *v and cleared (the stream is idle)
 int take_status_attention(int32_t *v);

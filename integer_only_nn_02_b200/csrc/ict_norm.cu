@@ -757,18 +757,24 @@ void finish_plan(NormArgs &a) {
     a.gso = a.fast ? __builtin_ctz((unsigned)a.gvo) : 0;
 }
 
-template <typename K>
-int run_rows(K kernel, const NormArgs &a, int lanes, size_t smem, cudaStream_t s) {
-    int sms = 0, per = 0;
+template <auto Kernel>
+int run_rows(const NormArgs &a, int lanes, size_t smem, cudaStream_t s) {
+    static std::atomic<uint64_t> fits[64];  // per device: shared memory asked for last, and how many blocks fit
+    int sms = 0, dev = 0;
     int st;
     if ((st = host::device_info(&sms))) return st;
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return ICT_ERR_CUDA;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, 256, smem) != cudaSuccess || per < 1)
-        return ICT_ERR_CUDA;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ICT_ERR_CUDA;
+    uint64_t f = fits[dev].load(std::memory_order_relaxed);
+    if (f >> 16 != smem || f == 0) {
+        int per = 0;
+        if (smem > 48 * 1024 && (st = host::allow_smem<Kernel>((int)smem))) return st;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, 256, smem) != cudaSuccess || per < 1) return ICT_ERR_CUDA;
+        f = (uint64_t)smem << 16 | (uint64_t)per;
+        fits[dev].store(f, std::memory_order_relaxed);
+    }
+    const int per = (int)(f & 0xffff);
     const int64_t blocks = std::min<int64_t>(host::cdiv(a.rows, 256 / lanes), (int64_t)sms * per);
-    kernel<<<(unsigned)blocks, 256, smem, s>>>(a);
+    Kernel<<<(unsigned)blocks, 256, smem, s>>>(a);
     host::counted(1);
     return host::launch_status();
 }
@@ -807,7 +813,7 @@ int32_t ict_layernorm_fwd(const ict_tensor *X, const ict_tensor *gamma, const ic
         constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
         finish_plan<L>(a);
         const size_t smem = (size_t)a.N * 8 + (a.fast ? 0 : (size_t)(256 / L) * a.ngo * 4);
-        st = run_rows(norm_fwd_kernel<L, V>, a, L, smem, s);
+        st = run_rows<norm_fwd_kernel<L, V>>(a, L, smem, s);
     });
     return st;
 }
@@ -843,7 +849,7 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
             constexpr int L = decltype(lanes)::value, V = decltype(vecs)::value;
             finish_plan<L>(a);
             const size_t smem = (size_t)a.N * 4 + (a.fast ? 0 : (size_t)(256 / L) * a.ngo * 4);
-            st = run_rows(norm_bwd_kernel<L, V>, a, L, smem, s);
+            st = run_rows<norm_bwd_kernel<L, V>>(a, L, smem, s);
         });
         if (st) return st;
         int sms = 0;

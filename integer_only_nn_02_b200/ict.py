@@ -172,6 +172,14 @@ class DevCE:
         return DevCE(mant, exp, g_rows, g_cols, cols=cols)
 
     @staticmethod
+    def near(t: torch.Tensor, rows, cols, g_cols):
+        """empty() with rows of (1, g_cols) groups, on the device of the mantissas or exponents t (which costs the
+        host less than naming the device)."""
+        g_cols = max(1, min(g_cols, cols)) if cols else max(1, g_cols)
+        ld = -(-cols // 16) * 16 if cols else 16
+        return DevCE(t.new_empty((rows, ld)), t.new_empty((rows, cdiv(cols, g_cols))), 1, g_cols, cols=cols)
+
+    @staticmethod
     def from_host(t: CE, device="cuda", pin=False):
         rows, cols = t.rows, t.cols
         ld = -(-cols // 16) * 16 if cols else 16
@@ -490,9 +498,12 @@ def ict_attention_bwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, len
                                  _stats(stats, c), dq, dk, dv, _ptr(ws), nbytes, _stream(stream)), "ict_attention_bwd")
 
 
+_VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
 def ict_values(t: DevCE, out: torch.Tensor, stream=None):
-    bf16 = {torch.float32: 0, torch.bfloat16: 1}[out.dtype]
-    assert out.is_cuda and tuple(out.shape) == (t.rows, t.cols) and (t.cols <= 1 or out.stride(1) == 1)
+    bf16 = _VALUE_TYPES[out.dtype]
+    assert out.is_cuda and out.shape == (t.rows, t.cols) and (t.cols <= 1 or out.stride(1) == 1)
     (r,) = _refs(t)
     _check(lib.ict_values(r, bf16, _ptr(out), out.stride(0) if t.rows > 1 else max(t.cols, 1), _stream(stream)),
            "ict_values")
@@ -627,28 +638,27 @@ def _on(stream):
 
 def layernorm_fwd(X: DevCE, gamma: DevCE, beta: DevCE | None = None, eps=(1, 20), g_cols=32, stream=None) -> DevCE:
     with _on(stream):
-        Y = DevCE.empty(X.rows, X.cols, 1, g_cols, X.mant.device)
+        Y = DevCE.near(X.mant, X.rows, X.cols, g_cols)
         ict_layernorm_fwd(X, gamma, beta, eps, Y)
     return Y
 
 
 def layernorm_bwd(X: DevCE, gamma: DevCE, dY: DevCE, eps=(1, 20), g_cols=32, stream=None):
     """(dX, dgamma, dbeta), all in (1, g_cols) groups."""
-    dev = X.mant.device
     with _on(stream):
-        dX = DevCE.empty(X.rows, X.cols, 1, g_cols, dev)
-        dg, db = DevCE.empty(1, X.cols, 1, g_cols, dev), DevCE.empty(1, X.cols, 1, g_cols, dev)
-        ict_layernorm_bwd(X, gamma, dY, eps, dX, dg, db, _ws(ict_layernorm_bwd_workspace(X), dev))
+        dX = DevCE.near(X.mant, X.rows, X.cols, g_cols)
+        dg, db = DevCE.near(X.mant, 1, X.cols, g_cols), DevCE.near(X.mant, 1, X.cols, g_cols)
+        ict_layernorm_bwd(X, gamma, dY, eps, dX, dg, db, X.mant.new_empty(ict_layernorm_bwd_workspace(X)))
     return dX, dg, db
 
 
 def attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, g_cols=32, lens_q=None, lens_k=None, stream=None):
     """(O [batch * len_q, heads_q * head_dim] in (1, g_cols) groups, stats for the backward pass).  See attn_desc for d."""
-    dev, c = Q.mant.device, attn_desc(d)
+    c = attn_desc(d)
     with _on(stream):
-        O = DevCE.empty(c.batch * c.len_q, c.heads_q * c.head_dim, 1, g_cols, dev)
-        stats = torch.empty((c.batch * c.heads_q * c.len_q, 2), dtype=torch.int32, device=dev)
-        ict_attention_fwd(c, Q, K, V, lens_q, lens_k, O, stats, _ws(ict_attention_workspace(False, c), dev))
+        O = DevCE.near(Q.mant, c.batch * c.len_q, c.heads_q * c.head_dim, g_cols)
+        stats = Q.mant.new_empty((c.batch * c.heads_q * c.len_q, 2), dtype=torch.int32)
+        ict_attention_fwd(c, Q, K, V, lens_q, lens_k, O, stats, Q.mant.new_empty(ict_attention_workspace(False, c)))
     return O, stats
 
 
@@ -660,22 +670,23 @@ def attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, O: DevCE, dO: DevCE, st
 
     def like(t: DevCE) -> DevCE:
         if id(t) not in made:
-            made[id(t)] = DevCE.empty(t.rows, t.cols, 1, g_cols, t.mant.device)
+            made[id(t)] = DevCE.near(t.mant, t.rows, t.cols, g_cols)
         return made[id(t)]
 
     c = attn_desc(d)
     with _on(stream):
         dQ, dK, dV = like(Q), like(K), like(V)
         ict_attention_bwd(c, Q, K, V, lens_q, lens_k, O, dO, stats, dQ, dK, dV,
-                          _ws(ict_attention_workspace(True, c), Q.mant.device))
+                          Q.mant.new_empty(ict_attention_workspace(True, c)))
     return dQ, dK, dV
 
 
 def values(t: DevCE, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values C 2^e of t [rows, cols]."""
     with _on(stream):
-        out = torch.empty((t.rows, t.cols), dtype=dtype, device=t.mant.device)
-        ict_values(t, out)
+        out = t.mant.new_empty((t.rows, t.cols), dtype=dtype)
+        (r,) = _refs(t)
+        _check(lib.ict_values(r, _VALUE_TYPES[dtype], out.data_ptr(), max(t.cols, 1), _stream()), "ict_values")
     return out
 
 
