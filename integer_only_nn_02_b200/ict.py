@@ -435,6 +435,15 @@ def _refs(*tensors: DevCE | None):
     return refs
 
 
+def _here(t: torch.Tensor | None):
+    """A plain tensor's address for a call that runs on the current device."""
+    if t is None:
+        return None
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    return t.data_ptr()
+
+
 def ict_layernorm_fwd(X: DevCE, gamma: DevCE, beta: DevCE | None, eps, Y: DevCE, stream=None):
     """eps = (mul, shift): the variance's epsilon mul 2^-shift."""
     x, g, b, y = _refs(X, gamma, beta, Y)
@@ -449,7 +458,7 @@ def ict_layernorm_bwd(X: DevCE, gamma: DevCE, dY: DevCE, eps, dX: DevCE, dgamma:
                       stream=None):
     nbytes = 0 if ws is None else ws.numel()
     x, g, dy, dx, dg, db = _refs(X, gamma, dY, dX, dgamma, dbeta)
-    _check(lib.ict_layernorm_bwd(x, g, dy, eps[0], eps[1], dx, dg, db, _ptr(ws), nbytes, _stream(stream)),
+    _check(lib.ict_layernorm_bwd(x, g, dy, eps[0], eps[1], dx, dg, db, _here(ws), nbytes, _stream(stream)),
            "ict_layernorm_bwd")
 
 
@@ -465,8 +474,8 @@ def attn_desc(d: dict | ict_attn_desc) -> ict_attn_desc:
 
 def _lens(t: torch.Tensor | None, batch: int):
     if t is not None:
-        assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous() and t.numel() == batch
-    return _ptr(t)
+        assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == batch
+    return _here(t)
 
 
 def ict_attention_workspace(backward: bool, d: dict | ict_attn_desc) -> int:
@@ -474,9 +483,8 @@ def ict_attention_workspace(backward: bool, d: dict | ict_attn_desc) -> int:
 
 
 def _stats(t: torch.Tensor, c: ict_attn_desc):
-    assert t.dtype == torch.int32 and t.is_cuda and t.is_contiguous()
-    assert t.numel() == 2 * c.batch * c.heads_q * c.len_q
-    return _ptr(t)
+    assert t.dtype == torch.int32 and t.is_contiguous() and t.numel() == 2 * c.batch * c.heads_q * c.len_q
+    return _here(t)
 
 
 def ict_attention_fwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE,
@@ -486,7 +494,7 @@ def ict_attention_fwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, len
     nbytes = 0 if ws is None else ws.numel()
     q, k, v, o = _refs(Q, K, V, O)
     _check(lib.ict_attention_fwd(ctypes.byref(c), q, k, v, _lens(lens_q, c.batch), _lens(lens_k, c.batch), o,
-                                 _stats(stats, c), _ptr(ws), nbytes, _stream(stream)), "ict_attention_fwd")
+                                 _stats(stats, c), _here(ws), nbytes, _stream(stream)), "ict_attention_fwd")
 
 
 def ict_attention_bwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, lens_q, lens_k, O: DevCE, dO: DevCE,
@@ -495,7 +503,7 @@ def ict_attention_bwd(d: dict | ict_attn_desc, Q: DevCE, K: DevCE, V: DevCE, len
     nbytes = 0 if ws is None else ws.numel()
     q, k, v, o, do, dq, dk, dv = _refs(Q, K, V, O, dO, dQ, dK, dV)
     _check(lib.ict_attention_bwd(ctypes.byref(c), q, k, v, _lens(lens_q, c.batch), _lens(lens_k, c.batch), o, do,
-                                 _stats(stats, c), dq, dk, dv, _ptr(ws), nbytes, _stream(stream)), "ict_attention_bwd")
+                                 _stats(stats, c), dq, dk, dv, _here(ws), nbytes, _stream(stream)), "ict_attention_bwd")
 
 
 _VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
@@ -503,9 +511,9 @@ _VALUE_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 def ict_values(t: DevCE, out: torch.Tensor, stream=None):
     bf16 = _VALUE_TYPES[out.dtype]
-    assert out.is_cuda and out.shape == (t.rows, t.cols) and (t.cols <= 1 or out.stride(1) == 1)
+    assert out.shape == (t.rows, t.cols) and (t.cols <= 1 or out.stride(1) == 1)
     (r,) = _refs(t)
-    _check(lib.ict_values(r, bf16, _ptr(out), out.stride(0) if t.rows > 1 else max(t.cols, 1), _stream(stream)),
+    _check(lib.ict_values(r, bf16, _here(out), out.stride(0) if t.rows > 1 else max(t.cols, 1), _stream(stream)),
            "ict_values")
 
 

@@ -286,6 +286,62 @@ def test_few_long_key_blocks(ict, case):
     status_ok(ict)
 
 
+def test_few_long_key_blocks_replayed(ict):
+    """Two captured graphs of shared key blocks, replayed in turn with an eager call between: the counters and sums
+    that the parts meet in are cleared by every call."""
+    m = _operators()
+    st = [m.prepare(dict(op="attn_bwd", B=1, Hq=4, Hkv=2, Lq=600, Lk=L, D=64, causal=True, ragged=False, packed=False, G=32), 5)
+          for L in (600, 300)]
+    m.own = True
+    want = [[t.clone() for t in m.run(k)] for k in st]
+    outs = [{}, {}]
+    graphs = [ict.StepGraph(lambda k=k: outs[k].update(r=m.run(st[k]))) for k in (0, 1)]
+    for _ in range(3):
+        for k in (0, 1):
+            for t in outs[k]["r"]:
+                t.zero_()
+            graphs[k].replay()
+            eager = m.run(st[1 - k])
+            torch.cuda.synchronize()
+            for x, y, z in zip(outs[k]["r"], want[k], range(9)):
+                assert torch.equal(x, y), (k, z)
+            for x, y in zip(eager, want[1 - k]):
+                assert torch.equal(x, y)
+    status_ok(ict)
+
+
+def test_lengths_outside_the_range(ict):
+    """Lengths are clamped to [0, len]."""
+    c = Case(6, 3, 2, 2, 40, 50, 64, True, [40, 1000, -3], [-1, 50, 2000])
+    a, lens = c.gpu(ict, 16), c.lens
+    c.lens = [np.clip(t, 0, n).astype(np.int32) for t, n in zip(lens, (40, 50))]
+    c.check(ict, 16)
+    for x, y in zip(a, c.gpu(ict, 16)):
+        for p, q in ((x, y),) if isinstance(x, torch.Tensor) else ((x.mant, y.mant), (x.exp, y.exp)):
+            assert torch.equal(p, q)
+
+
+def test_tensors_elsewhere_are_refused(ict):
+    """Plain tensors that a kernel would read or write at an address of another device."""
+    c = Case(1, 1, 1, 1, 8, 8, 16)
+    q = ict.DevCE.from_host(c.Q)
+    o, stats = ict.attention_fwd(c.d, q, q, q, 16)
+    host = torch.tensor([8], dtype=torch.int32)
+    for lens in ((host, None), (None, host)):
+        with pytest.raises(ValueError):
+            ict.attention_fwd(c.d, q, q, q, 16, *lens)
+    ws = torch.empty(ict.ict_attention_workspace(False, c.d), dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        ict.ict_attention_fwd(c.d, q, q, q, None, None, o, stats, ws)
+    with pytest.raises(ValueError):
+        ict.ict_attention_fwd(c.d, q, q, q, None, None, o, stats.cpu(), ws.cuda())
+    with pytest.raises(ValueError):
+        ict.attention_bwd(c.d, q, q, q, o, o, stats.cpu(), 16)
+    with pytest.raises(ValueError):
+        ict.ict_values(o, torch.empty((8, 16), dtype=torch.bfloat16))
+    status_ok(ict)
+
+
 def test_streams_and_graph(ict):
     """The same calls on two streams at once and as one replayed graph: a transformer layer's norm, attention and
     both backward passes, each with its own workspace."""
