@@ -65,7 +65,7 @@ __device__ __forceinline__ void copy_rows(const AttnArgs &a, const OperandRows &
 }
 
 constexpr int kTopRows = 128;      // rows of a block of the two-kernel form
-constexpr int kFuseVecs = 8192;    // at most this many vectors per operand and key/value head: one kernel
+constexpr int kFuseVecs = 2048;    // see align_operands
 
 // Largest group exponent of every operand's valid rows, per sequence and key/value head
 // (a.top, very negative before).  Grid (row block, sequence and head, operand).
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) attn_copy_kernel(const __grid_constant__ 
 }
 // Both in one kernel, a block per sequence, key/value head and operand: the exponents are
 // scanned by the block that copies.  One launch and one pass instead of a memset and two
-// launches; for heads of 197 x 64 the three operands of 768 heads take 11 us against 36 us.
+// launches; for heads of 197 x 64 the three operands of 768 heads take 17 us against 34 us.
 template <int NV>
 __global__ void __launch_bounds__(256) attn_align_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ int m;
@@ -203,13 +203,26 @@ int check_out(const ict_tensor *t, int64_t rows, int col, int64_t width, int D) 
     return ICT_OK;
 }
 
-// Few key blocks leave SMs without work, and causal ones differ in length: their queries are then
-// shared by up to kSplitTarget / blocks parts of at least kSplitTiles tiles.
-constexpr int kSplitTarget = 4 * 148, kSplitTiles = 4;
+// Few key blocks leave SMs without work, and causal ones differ in length: the queries of a key
+// block are then shared by parts whose sums are joined.  The time in tiles of 128 queries (2.2 us):
+// a block of threads costs about 3 beside its tiles, a part 6 and 0.6 for every part that the last
+// one adds up; blocks run in waves, unequal (causal) ones as SMs become free.  Heads of 64 columns,
+// one part against the chosen number: 3 x 8 causal heads of 2048 tokens on 2, 144 us against 81 us;
+// 3 causal heads of 4096, 77 against 52 us; 8 heads of 512 on one, 75 against 31 us.  Where one
+// part is chosen, two cost more: 12 heads of 1024 tokens 25 against 42 us, causal 24 against 28 us.
 int split_parts(const AttnArgs &a) {
-    if (a.blocks == 0) return 1;
-    const int64_t tiles = host::cdiv(a.Lq, 128) * a.rep;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kSplitTarget / a.blocks, tiles / kSplitTiles));
+    const double tiles = (double)host::cdiv(a.Lq, 128) * a.rep, blocks = a.blocks, sms = 148;
+    // of the queries, those that a key sees on average
+    const double mean = a.Lk <= a.Lq ? (double)a.Lk / (2.0 * std::max(a.Lq, 1)) : 1.0 - (double)a.Lq / (2.0 * a.Lk);
+    int best = 1;
+    double least = 0;
+    for (int p = 1; p <= 32 && (p == 1 || 2 * p <= tiles); ++p) {
+        const double beside = p == 1 ? 3 : 6 + 0.6 * p, longest = tiles / p + beside, n = blocks * p;
+        const double all = a.causal ? n * (tiles * mean / p + beside) / sms : 0;
+        const double t = a.causal ? std::max(longest, all) : std::ceil(n / sms) * longest;
+        if (p == 1 || t < 0.9 * least) best = p, least = t;
+    }
+    return best;
 }
 
 Div divide_by(int d) {  // d >= 1
@@ -253,7 +266,7 @@ bool few_queries_path(const AttnArgs &a, bool back) {
 struct Scratch {
     size_t top, copy[OPN], row, tmax, total;
     size_t scores, mx, sum, acc;  // the few-queries path (scores apart, the others cleared before use)
-    size_t exps, join, tickets;   // backward (tickets and join are cleared before use)
+    size_t exps, join, tickets;   // backward (tickets are cleared before use)
 };
 Scratch scratch(const AttnArgs &a, bool back) {
     Scratch s = {};
@@ -284,7 +297,7 @@ Scratch scratch(const AttnArgs &a, bool back) {
     if (back && a.parts > 1) {
         const int64_t n = (int64_t)a.blocks * (a.Dp / 64);
         s.tickets = take(n * 4);
-        s.join = take(n * 256 * 128 * 4);
+        s.join = take(n * a.parts * kPartSums * 16);
     }
     s.total = at;
     return s;
@@ -328,8 +341,10 @@ int align_operands(const AttnArgs &a, cudaStream_t s) {
     const int L = std::max(a.Lq, a.Lk);
     const int64_t vecs = std::max((int64_t)a.rep * a.Lq, (int64_t)a.Lk) * NV;
     const unsigned bg = (unsigned)(a.B * a.Hkv);
-    // a few iterations per thread, or enough heads to fill the SMs
-    if (vecs <= kFuseVecs || (bg >= 148 && vecs <= 4 * kFuseVecs)) {
+    // Few vectors per block of threads, or enough heads to fill the SMs: one kernel.  12 heads of 64
+    // columns: 512 rows 7.0 us against 6.7 us in three launches, 1024 rows 11.9 against 6.9; 192 heads:
+    // 1024 rows 30 against 38 us, 2048 rows 58 against 68 us.
+    if (vecs <= kFuseVecs || (bg >= 148 && vecs <= 16 * kFuseVecs)) {
         attn_align_kernel<NV><<<dim3(bg, (unsigned)a.n_op), 256, 0, s>>>(a);
         host::counted(1);
         return host::launch_status();
@@ -430,9 +445,7 @@ int launch_bwd(const AttnArgs &a, cudaStream_t s) {
         attn_exps_kernel<<<(unsigned)a.blocks, threads, 0, s>>>(a);
         host::counted(1);
         if (a.parts > 1) {
-            const int64_t n = (int64_t)a.blocks * (DP / 64);
-            if (cudaMemsetAsync(a.tickets, 0, (size_t)((uint8_t *)(a.join + n * 256 * 128) - (uint8_t *)a.tickets), s) != cudaSuccess)
-                return ICT_ERR_CUDA;
+            if (cudaMemsetAsync(a.tickets, 0, (size_t)a.blocks * (DP / 64) * 4, s) != cudaSuccess) return ICT_ERR_CUDA;
         }
         if constexpr (DP == 64) {
             if ((st = host::allow_smem<attn_dkv_kernel<64, 3>>(L::kBytes))) return st;
@@ -514,7 +527,7 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     a.row = (int2 *)(base + w.row);
     a.tmax = (int32_t *)(base + w.tmax);
     a.exps = (int4 *)(base + w.exps);
-    if (a.parts > 1) a.tickets = (int32_t *)(base + w.tickets), a.join = (int32_t *)(base + w.join);
+    if (a.parts > 1) a.tickets = (int32_t *)(base + w.tickets), a.join = (uint4 *)(base + w.join);
     if (rq == 0 && rk == 0) return ICT_OK;
     cudaStream_t s = (cudaStream_t)stream;
     const int64_t rows = rq * a.Hq;

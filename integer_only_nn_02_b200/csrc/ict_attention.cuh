@@ -54,7 +54,8 @@ struct AttnArgs {
     AttnOut dk, dv;
     int4 *exps;          // [key blocks * B * Hkv]: pi, c, exponents of the sums of dV and dK
     int parts, blocks;   // each key block's queries are shared by so many; key blocks * B * Hkv
-    int32_t *join, *tickets;  // with parts > 1: their sums, and how many have added theirs
+    uint4 *join;         // with parts > 1: their sums
+    int32_t *tickets;    // and how many have left theirs
 };
 
 __device__ __forceinline__ int clamp_len(const int32_t *lens, int b, int L) {
