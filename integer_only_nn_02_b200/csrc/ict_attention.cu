@@ -220,7 +220,7 @@ int split_parts(const AttnArgs &a) {
         const double beside = p == 1 ? 3 : 6 + 0.6 * p, longest = tiles / p + beside, n = blocks * p;
         const double all = a.causal ? n * (tiles * mean / p + beside) / sms : 0;
         const double t = a.causal ? std::max(longest, all) : std::ceil(n / sms) * longest;
-        if (p == 1 || t < 0.9 * least) best = p, least = t;
+        if (p == 1 || t < (best == 1 ? 0.9 : 1.0) * least) best = p, least = t;
     }
     return best;
 }
