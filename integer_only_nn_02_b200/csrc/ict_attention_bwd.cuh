@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar_of + 8 * turn, (on >> 1) & 1, lim.wait_ns, abort_flag));
             tc_fence_after();
             float2 *gm = (float2 *)(smem + L::kOffRed) + turn * 8 * 128 + et;
-            fit_row_tmem<DP / 32>(a, a.o, out, (wg & 1) * (DP / 2), r, w.nk <= 1024, gm, 128, 1 + turn, NS / 2,
+            fit_row_tmem<DP / 32>(a, a.o, out, (wg & 1) * (DP / 2), r, w.nk <= 1024, gm, (int *)(gm - et) + et, 128, 1 + turn, NS / 2,
                                   AccCols{tm + lanes + L::kAcc, DP, ok}, bar_oe);
             ++on;
         }
@@ -373,8 +373,8 @@ struct DkvCfg {
     static constexpr int kOffQ = KS * 2 * kTile;                           // K stage: K tile, V tile; Q stage: Q tile, dO tile
     static constexpr int kVec = 3 * kStep + 4;                             // a step's floats: see dkv16, then f and 2^-c
     static constexpr int kOffVec = kOffQ + QS * 2 * kTile;                 // [4][kVec] floats
-    static constexpr int kOffRed = kOffVec + 4 * kVec * 4;                 // [8][128] float2
-    static constexpr int kOffBar = kOffRed + 8 * 128 * 8;
+    static constexpr int kOffRed = kOffVec + 4 * kVec * 4;                 // [8][128] float2, [2][8][128] int
+    static constexpr int kOffBar = kOffRed + 8 * 128 * 8 + 2 * 8 * 128 * 4;
     static constexpr int kBars = 2 * (KS + QS) + 2 + 2 + 4 + 4 + 5;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 96;
@@ -825,8 +825,11 @@ __global__ void __launch_bounds__(DkvCfg<DP>::kThreads, 1)
                     continue;
                 }
             }
-            float2 *gm = (float2 *)(smem + L::kOffRed) + (MODE == 3 && is_k ? 4 * 128 : 0) + et;
-            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, out, cc, is_k ? ex.w : ex.z, (int64_t)w.nq * a.rep <= 1024, gm, 128,
+            const int half = (MODE == 3 && is_k ? 4 * 128 : 0) + et;
+            float2 *gm = (float2 *)(smem + L::kOffRed) + half;
+            // two of these in turn: a warp may read its group's maxima after the accumulators are released
+            int *gi = (int *)(smem + L::kOffRed + 8 * 128 * 8) + (on & 1) * 8 * 128 + half;
+            fit_row_tmem<2>(a, is_k ? a.dk : a.dv, out, cc, is_k ? ex.w : ex.z, (int64_t)w.nq * a.rep <= 1024, gm, gi, 128,
                             MODE == 3 ? 2 + (wg >> 1) : 1, MODE == 3 ? NS / 2 : NS, sums, bar_oe);
         }
         if (!ok && lane == 0) fail();

@@ -181,72 +181,113 @@ __device__ __noinline__ uint4 exact_round16(const int *x, uint4 w, int e, float 
     return w;
 }
 
-// FIT of 16 SEGS columns in groups of one or two segments: 32 columns at a time stay in registers
-// between the maximum and the rounding, and the accumulators are free for the next item once the
-// last of them are read.
+// 32 columns of a row as whole numbers (narrow accumulators), and the largest magnitude of each half.
+__device__ __forceinline__ void load32(const AccCols &acc, int c, int (&x)[32], int (&m)[2]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        uint32_t hi[16], lo[16];
+        acc.load16(c + 16 * s, hi, lo);
+        int top = 0, low = 0;
+#pragma unroll
+        for (int q = 0; q < 16; q += 2) {
+            x[16 * s + q] = (int)hi[q] * 256 + (int)lo[q];
+            x[16 * s + q + 1] = (int)hi[q + 1] * 256 + (int)lo[q + 1];
+            top = __vimax3_s32(top, x[16 * s + q], x[16 * s + q + 1]);
+            low = __vimin3_s32(low, x[16 * s + q], x[16 * s + q + 1]);
+        }
+        m[s] = max(top, -low);
+    }
+}
+// Exponent, factor and border of a group whose largest magnitude is mi.
+__device__ __forceinline__ GroupFit group_fit_narrow(int mi, bool some, float rd, int den, int mul, int r) {
+    GroupFit f;
+    // four roundings: the magnitude, the divisor, the factor, the product
+    const float w = (float)mi, q0 = w * rd, dq = q0 * 4.76837158203125e-07f;  // 2^-21
+    const bool zero = !some || mi == 0;
+    const int n0 = zero ? 0 : need_rel_f32(__float_as_uint(fmaxf(q0 - dq, 1.17549435e-38f)), 8);
+    int need = zero ? 0 : need_rel_f32(__float_as_uint(q0 + dq), 8);
+    if (n0 != need) need = exact_need(mi, mul, den);
+    f.e = zero ? kEZero : finalize_exp(need + r);
+    f.sc = zero ? 0.0f : rd * pow2f(min(max(r - f.e, -126), 100));
+    // three roundings: w sc 2^-22; none at all (ties included) where den is 1 and every value below 2^24
+    f.lim = den == 1 && mi < (1 << 24) ? 1.0f : fmaf(w * f.sc, -2.38418579e-07f, 0.4999999f);
+    return f;
+}
+// 16 mantissas x mul / den 2^(r - e).
+__device__ __forceinline__ uint4 round16_narrow(const int *x, const GroupFit &f, int r, int mul, int den) {
+    const f2 M = pk(kAttnMagic), scp = pk(f.sc);
+    uint32_t v[16];
+    float far = 0;  // from a whole number
+#pragma unroll
+    for (int q = 0; q < 16; q += 2) {
+        const f2 n = pk((float)x[q], (float)x[q + 1]), w = fma2(n, scp, M);
+        float w0, w1, d0, d1;
+        unpk(w, w0, w1);
+        unpk(fma2(n, scp, sub2(M, w)), d0, d1);  // what the rounding took away
+        far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
+        v[q] = __float_as_uint(w0), v[q + 1] = __float_as_uint(w1);
+    }
+    uint4 w = make_uint4(pack4b(v[0], v[1], v[2], v[3]), pack4b(v[4], v[5], v[6], v[7]), pack4b(v[8], v[9], v[10], v[11]),
+                         pack4b(v[12], v[13], v[14], v[15]));
+    if (!(far < f.lim) || f.e == 127) {
+        int y[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) y[q] = x[q];
+        w = exact_round16(y, w, f.e, f.sc, f.lim, r, mul, den);
+    }
+    return w;
+}
+
+// FIT of 16 SEGS columns of narrow accumulators, 32 columns at a time in registers.  Groups of one or
+// two segments lie inside them; the maxima of others meet in gi (shared memory, [segment][stride]),
+// and with more than 32 columns the accumulators are read twice.  They are free for the next item
+// once the last of them are read.
 template <int SEGS>
-__device__ __forceinline__ void fit_row_regs(const AttnArgs &a, int8_t *dst, int8_t *oe, int c0, int gs, int den, int mul,
-                                             int r, bool live, bool some, float rd, const AccCols &acc, uint32_t release) {
-    const f2 M = pk(kAttnMagic);
+__device__ __forceinline__ void fit_row_narrow(const AttnArgs &a, int8_t *dst, int8_t *oe, int c0, int gs, int den, int mul,
+                                               int r, bool live, bool some, float rd, int *gi, int stride, int bar,
+                                               int nthreads, const AccCols &acc, uint32_t release) {
+    static_assert(SEGS % 2 == 0, "32 columns at a time");
+    const bool meet = gs > 2;
+    int x[32], m[2];
+    if (meet) {
+#pragma unroll 1
+        for (int h = 0; h < SEGS; h += 2) {
+            load32(acc, c0 + 16 * h, x, m);
+            gi[(c0 / 16 + h) * stride] = m[0];
+            gi[(c0 / 16 + h + 1) * stride] = m[1];
+        }
+        if (SEGS == 2 && release) warp_arrive(release);
+        named_bar_sync(bar, nthreads);
+    }
 #pragma unroll 1
     for (int h = 0; h < SEGS; h += 2) {
         const int c = c0 + 16 * h;
-        int x[32], m[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            uint32_t hi[16], lo[16];
-            acc.load16(c + 16 * s, hi, lo);
-            int top = 0, low = 0;
-#pragma unroll
-            for (int q = 0; q < 16; q += 2) {
-                x[16 * s + q] = (int)hi[q] * 256 + (int)lo[q];
-                x[16 * s + q + 1] = (int)hi[q + 1] * 256 + (int)lo[q + 1];
-                top = __vimax3_s32(top, x[16 * s + q], x[16 * s + q + 1]);
-                low = __vimin3_s32(low, x[16 * s + q], x[16 * s + q + 1]);
-            }
-            m[s] = max(top, -low);
+        if (!meet || SEGS > 2) {
+            load32(acc, c, x, m);
+            if (release && h + 2 >= SEGS) warp_arrive(release);
         }
-        if (release && h + 2 >= SEGS) warp_arrive(release);
-        int e = kEZero;
-        float sc = 0.0f, lim = 0.5f;
+        GroupFit f{kEZero, 0.0f, 0.5f};
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            if (c + 16 * s >= a.D) break;
-            if (s == 0 || gs == 1) {
-                const int mi = gs == 1 ? m[s] : max(m[0], m[1]);
-                // four roundings: the magnitude, the divisor, the factor, the product
-                const float w = (float)mi, q0 = w * rd, dq = q0 * 4.76837158203125e-07f;  // 2^-21
-                const bool zero = !some || mi == 0;
-                const int n0 = zero ? 0 : need_rel_f32(__float_as_uint(fmaxf(q0 - dq, 1.17549435e-38f)), 8);
-                int need = zero ? 0 : need_rel_f32(__float_as_uint(q0 + dq), 8);
-                if (n0 != need) need = exact_need(mi, mul, den);
-                e = zero ? kEZero : finalize_exp(need + r);
-                sc = zero ? 0.0f : rd * pow2f(min(max(r - e, -126), 100));
-                // three roundings: w sc 2^-22; none at all (ties included) where den is 1 and every value below 2^24
-                lim = den == 1 && mi < (1 << 24) ? 1.0f : fmaf(w * sc, -2.38418579e-07f, 0.4999999f);
-                if (live) oe[(c + 16 * s) >> (3 + gs)] = (int8_t)e;  // 16 or 32 columns
+            const int seg = c / 16 + s;
+            if (16 * seg >= a.D) break;
+            int mi = gs == 1 ? m[s] : max(m[0], m[1]), g = seg >> (gs - 1);
+            bool first = s == 0 || gs == 1, writes = first;
+            if (meet) {
+                g = seg / gs;
+                writes = seg == g * gs;
+                first = s == 0 || writes;
+                if (first) {
+                    mi = 0;
+                    for (int k = g * gs; k < (g + 1) * gs; ++k) mi = max(mi, gi[k * stride]);
+                }
             }
-            const f2 scp = pk(sc);
-            uint32_t v[16];
-            float far = 0;  // from a whole number
-#pragma unroll
-            for (int q = 0; q < 16; q += 2) {
-                const f2 n = pk((float)x[16 * s + q], (float)x[16 * s + q + 1]), w = fma2(n, scp, M);
-                float w0, w1, d0, d1;
-                unpk(w, w0, w1);
-                unpk(fma2(n, scp, sub2(M, w)), d0, d1);  // what the rounding took away
-                far = fmaxf(far, fmaxf(fabsf(d0), fabsf(d1)));
-                v[q] = __float_as_uint(w0), v[q + 1] = __float_as_uint(w1);
+            if (first) {
+                f = group_fit_narrow(mi, some, rd, den, mul, r);
+                if (live && writes) oe[g] = (int8_t)f.e;
             }
-            uint4 w = make_uint4(pack4b(v[0], v[1], v[2], v[3]), pack4b(v[4], v[5], v[6], v[7]),
-                                 pack4b(v[8], v[9], v[10], v[11]), pack4b(v[12], v[13], v[14], v[15]));
-            if (!(far < lim) || e == 127) {
-                int y[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) y[q] = x[16 * s + q];
-                w = exact_round16(y, w, e, sc, lim, r, mul, den);
-            }
-            if (live) *reinterpret_cast<uint4 *>(dst + c + 16 * s) = w;
+            const uint4 w = round16_narrow(x + 16 * s, f, r, mul, den);
+            if (live) *reinterpret_cast<uint4 *>(dst + 16 * seg) = w;
         }
     }
 }
@@ -256,9 +297,8 @@ __device__ __forceinline__ void fit_row_regs(const AttnArgs &a, int8_t *dst, int
 // Magnitudes and mantissas are computed in fp32 with an error bound; what lies within the bound
 // of a border between two results (a mantissa in some ten thousand) is decided in fp64, where
 // the quotient's rounding to 53 bits cannot hide the border.  narrow: the accumulators
-// 256 hi + lo fit 32 bits; groups of 16 and 32 columns then stay in registers.  For other
-// groups the threads that share the row join their segments' maxima in gmax (shared memory,
-// [segment][stride]) and read the accumulators twice.
+// 256 hi + lo fit 32 bits (gi: see above).  Otherwise the threads that share the row join their
+// segments' maxima in gmax (shared memory, [segment][stride]) and read the accumulators twice.
 struct RowOut {  // what is known of a row before its accumulators are complete
     int8_t *dst, *oe;
     float rd;
@@ -276,15 +316,15 @@ __device__ __forceinline__ RowOut row_out(const AttnArgs &a, const AttnOut &out,
 }
 template <int SEGS>
 __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &out, const RowOut &o, int c0, int r, bool narrow,
-                                             float2 *gmax, int stride, int bar, int nthreads, const AccCols &acc,
+                                             float2 *gmax, int *gi, int stride, int bar, int nthreads, const AccCols &acc,
                                              uint32_t release) {
     const int gs = out.G / 16;  // segments of a group
     const float rd = o.rd;
     const int den = o.den, mul = o.mul;
     const bool live = o.live, some = o.some;
     int8_t *dst = o.dst, *oe = o.oe;
-    if (SEGS % 2 == 0 && gs <= 2 && narrow) {
-        fit_row_regs<SEGS>(a, dst, oe, c0, gs, den, mul, r, live, some, rd, acc, release);
+    if (narrow) {
+        fit_row_narrow<SEGS>(a, dst, oe, c0, gs, den, mul, r, live, some, rd, gi, stride, bar, nthreads, acc, release);
         return;
     }
 #pragma unroll 1
@@ -666,7 +706,7 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             // outputs: columns [wg DP / NWG, ...) of the head; every thread takes part in the barriers
             const int c0 = wg * (DP / NWG);
             float2 *gm = (float2 *)(smem + L::kOffRed + 2048) + et;
-            fit_row_tmem<DP / NWG / 16>(a, a.o, row, c0, top_v, w.nk <= 1024, gm, 128, 1, NS,
+            fit_row_tmem<DP / NWG / 16>(a, a.o, row, c0, top_v, w.nk <= 1024, gm, (int *)(gm - et) + et, 128, 1, NS,
                                         AccCols{tm + lanes + L::kO, DP, read}, w.nt > 0 ? bar_oe : 0);
             if (w.nt > 0) ++on;
         }
