@@ -9,7 +9,10 @@
 //   few_values_kernel  E from the true maximum, sum E, sum E AV (dp2a on pairs of keys)
 //   few_out_kernel     FIT of the quotients
 // Partial sums and maxima are whole numbers joined by integer atomics, so the split changes
-// nothing.  Bound by memory: one byte per element of K and V, 4 bytes per score written and read.
+// nothing.  Needed of memory: one byte per element of K and V, 4 bytes per score written and read
+// (21 us at the copy's rate for 16 sequences of up to 16384 keys, 4 heads of 64, 3 queries each).
+// Measured there: exponents 8 us, scores 22 us, values 32 us, quotients 5 us; bound by the
+// alignment of every vector to e* and the dp4a / dp2a (half of the issue slots), not by memory.
 #pragma once
 
 #include "ict_attention.cuh"

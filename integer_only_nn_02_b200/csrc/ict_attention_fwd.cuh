@@ -11,10 +11,12 @@
 // not depend on the order or the split of the work; that is why the maxima come first, and a
 // second S costs less than keeping or rescaling anything: the int8 contraction of a tile takes
 // 128 (64 columns) of the about 1300 cycles that its 16384 weights take on the other pipes.
-// Bound by the exponential unit (16 a cycle and SM) and the issue slots (6 instructions a
-// weight).  Two blocks per SM for heads up to 64 columns (256 TMEM columns each); one block with
-// two softmax warpgroups, each half a tile's columns, for wider heads.
-//   warps 0 .. 4 NWG - 1   softmax (thread = query row = TMEM lane)
+// Bound by the issue slots (6 instructions a weight beside the maxima) and the exponential unit
+// (16 a cycle and SM), and for short rows by an item's ends: 2 x 12 causal heads of 4096 tokens
+// and 64 columns 115 us (448 TFLOP/s of the contractions that are needed), 64 x 12 heads of 197
+// tokens 46 us (the rounding of the outputs and the items' starts count there).  Two blocks per SM
+// for heads up to 64 columns (256 TMEM columns each), one for wider heads.
+//   warps 0 .. 4 NWG - 1   softmax (thread = query row = TMEM lane; each warpgroup half the columns)
 //   next warp              TMA producer;  last warp: TMEM allocation and MMA issue
 // Every wait is bounded as in the Product kernels.
 #pragma once
