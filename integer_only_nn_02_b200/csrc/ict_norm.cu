@@ -113,28 +113,58 @@ __device__ __forceinline__ float row_scale(const NormArgs &p, int s1, int s2, in
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-template <int L>
-__device__ __forceinline__ int lanes_sum(int v) {
+// Reductions over the L lanes of a row.  Rows of more than a warp meet in shared memory, every thread
+// of the block at once; two buffers in turn, so that one barrier each is enough.
+struct RowRed {
+    long long *buf;  // [2][8 warps][2]
+    int turn;
+};
+template <int L, int K, typename T, typename Op>
+__device__ __forceinline__ void lanes_all(T (&v)[K], RowRed &red, const Op &op) {
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = (L < 32 ? L : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] = op(v[k], __shfl_xor_sync(0xffffffffu, v[k], o));
+    if constexpr (L > 32) {
+        T *s = reinterpret_cast<T *>(red.buf + red.turn * 16);
+        red.turn ^= 1;
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) s[(threadIdx.x >> 5) * 2 + k] = v[k];
+        }
+        __syncthreads();
+        const int w0 = (int)(threadIdx.x / L) * (L / 32);
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            v[k] = s[w0 * 2 + k];
+#pragma unroll
+            for (int w = 1; w < L / 32; ++w) v[k] = op(v[k], s[(w0 + w) * 2 + k]);
+        }
+    }
 }
+struct Sum {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct Max {
+    template <typename T>
+    __device__ __forceinline__ T operator()(T a, T b) const { return max(a, b); }
+};
 template <int L>
-__device__ __forceinline__ int lanes_max(int v) {
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+__device__ __forceinline__ void row_sync() {
+    if (L > 32) __syncthreads();
+    else __syncwarp();
 }
 
 // One row's vectors, aligned to the row's largest group exponent (returned; kNoExp when
 // every group is zero).  ex[v] is the group exponent of vector v.
 template <int L, int V>
-__device__ __forceinline__ int align_vectors(uint4 (&w)[V], const int (&ex)[V], const RneK *rk) {
-    int top = kNoExp;
+__device__ __forceinline__ int align_vectors(uint4 (&w)[V], const int (&ex)[V], const RneK *rk, RowRed &red) {
+    int tops[1] = {kNoExp}, &top = tops[0];
 #pragma unroll
     for (int v = 0; v < V; ++v)
         if (ex[v] != kEZero) top = max(top, ex[v]);
-    top = lanes_max<L>(top);
+    lanes_all<L>(tops, red, Max());
     bool shift = false;
 #pragma unroll
     for (int v = 0; v < V; ++v) shift |= ex[v] != kEZero && ex[v] != top;
@@ -226,7 +256,7 @@ __device__ __forceinline__ void fit_row(const NormArgs &p, int64_t row, bool liv
             uint32_t m = max16(y);
             if (q >= p.nvec) m = 0;
 #pragma unroll
-            for (int o = 1; o < L; o <<= 1)
+            for (int o = 1; o < (L < 32 ? L : 32); o <<= 1)
                 if (o < p.gvo) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             int e;
             const uint4 w = fit16(y, m, base, e);
@@ -238,7 +268,7 @@ __device__ __forceinline__ void fit_row(const NormArgs &p, int64_t row, bool liv
         return;
     }
     for (int g = lane_in_row; g < p.ngo; g += L) gmax[g] = 0;
-    __syncwarp();
+    row_sync<L>();
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
@@ -259,7 +289,7 @@ __device__ __forceinline__ void fit_row(const NormArgs &p, int64_t row, bool liv
                 }
             }
         }
-        __syncwarp();
+        row_sync<L>();
     }
 }
 
@@ -267,13 +297,14 @@ __device__ __forceinline__ void fit_row(const NormArgs &p, int64_t row, bool liv
 // Needs 2 bytes a value of memory; the row stays packed in registers between the sums and the
 // output, gamma and beta stay in shared memory as floats.  50432 x 768: 36 us, where memory alone
 // would take 12 us; bound by about 18 instructions a value (alignment, centring, scale, maximum,
-// rounding: the ALU pipe 41 % busy, half of the issue slots) and their latencies.  Rows above 4096
-// values spill registers (16 vectors a lane).
+// rounding: the ALU pipe 41 % busy, half of the issue slots) and their latencies.
 template <int L, int V>
-__global__ void __launch_bounds__(256, V <= 4 ? 3 : (V <= 8 ? 2 : 1)) norm_fwd_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(256, 3) norm_fwd_kernel(const __grid_constant__ NormArgs p) {
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ int top;
     __shared__ RneK rk[9];
+    __shared__ long long rbuf[32];
+    RowRed red{rbuf, 0};
     float4 *tg = reinterpret_cast<float4 *>(sm), *tb = tg + 4 * p.nvec;
     uint32_t *gm = reinterpret_cast<uint32_t *>(tb + 4 * p.nvec) + (threadIdx.x / L) * p.ngo;
     rne_table_init(rk);
@@ -316,8 +347,8 @@ __global__ void __launch_bounds__(256, V <= 4 ? 3 : (V <= 8 ? 2 : 1)) norm_fwd_k
                 if (v * L + lr < p.nvec) prefetch_l2(p.x + nx * p.ldx + (v * L + lr) * 16);
             if (lr == 0) prefetch_l2(p.x_exp + nx * p.ngx);
         }
-        const int e = align_vectors<L, V>(w, ex, rk);
-        int s1 = 0, s2 = 0;
+        const int e = align_vectors<L, V>(w, ex, rk, red);
+        int s12[2] = {0, 0}, &s1 = s12[0], &s2 = s12[1];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const uint32_t u[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
@@ -327,8 +358,7 @@ __global__ void __launch_bounds__(256, V <= 4 ? 3 : (V <= 8 ? 2 : 1)) norm_fwd_k
                 s2 = __dp4a((int)u[k], (int)u[k], s2);
             }
         }
-        s1 = lanes_sum<L>(s1);
-        s2 = lanes_sum<L>(s2);
+        lanes_all<L>(s12, red, Sum());
         const f2 N2 = pk((float)p.N), m1 = pk(-(float)s1), R2 = pk(row_scale(p, s1, s2, e) * 256.0f);
         const f2 mg = pk(kMagic), nmg = pk(-kMagic);
         fit_row<L, V>(p, row, live, lr, eb, gm, [&](int v, f2(&y)[8]) {
@@ -351,11 +381,13 @@ __global__ void __launch_bounds__(256, V <= 4 ? 3 : (V <= 8 ? 2 : 1)) norm_fwd_k
 // and the largest exponent of every column group of dY.  50432 x 768: 62 us (18 us of memory),
 // bound like the forward; h and g are formed twice, which costs less than keeping them.
 template <int L, int V>
-__global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(256, 2) norm_bwd_kernel(const __grid_constant__ NormArgs p) {
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ int top;
     __shared__ int cm[kMaxCols / 16];  // the block's largest exponent of every column group of dY
     __shared__ RneK rk[9];
+    __shared__ long long rbuf[32];
+    RowRed red{rbuf, 0};
     for (int g = threadIdx.x; g < p.ngd; g += blockDim.x) cm[g] = kNoExp;
     float4 *tg = reinterpret_cast<float4 *>(sm);
     uint32_t *gm = reinterpret_cast<uint32_t *>(tg + 4 * p.nvec) + (threadIdx.x / L) * p.ngo;
@@ -415,8 +447,8 @@ __global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __g
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (ed[v] != kEZero) ctop[v] = max(ctop[v], ed[v]);
-        const int e = align_vectors<L, V>(w, ex, rk), e2 = align_vectors<L, V>(d, ed, rk);
-        int s1 = 0, s2 = 0;
+        const int e = align_vectors<L, V>(w, ex, rk, red), e2 = align_vectors<L, V>(d, ed, rk, red);
+        int s12[2] = {0, 0}, &s1 = s12[0], &s2 = s12[1];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const uint32_t u[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
@@ -426,13 +458,12 @@ __global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __g
                 s2 = __dp4a((int)u[k], (int)u[k], s2);
             }
         }
-        s1 = lanes_sum<L>(s1);
-        s2 = lanes_sum<L>(s2);
+        lanes_all<L>(s12, red, Sum());
         const float R = row_scale(p, s1, s2, e);
         if (live && lr == 0) p.stat[row] = make_float4((float)s1, R, __int_as_float(e), 0.0f);
         const f2 N2 = pk((float)p.N), ms = pk(-(float)s1), R2 = pk(R * 256.0f), mg = pk(kMagic), nmg = pk(-kMagic);
         // S3 = sum g and S4 = sum g h: g in 16-bit halves, h in its two bytes
-        int s3 = 0, s4l = 0, s4h = 0;
+        int s3s[1] = {0}, &s3 = s3s[0], s4l = 0, s4h = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int q = min(v * L + lr, p.nvec - 1);
@@ -458,10 +489,9 @@ __global__ void __launch_bounds__(256, V <= 4 ? 2 : 1) norm_bwd_kernel(const __g
                 s4h = dp2a_lo_s(ga01, (int)hh, dp2a_hi_s(ga23, (int)hh, s4h));
             }
         }
-        s3 = lanes_sum<L>(s3);
-        int64_t s4 = (int64_t)s4h * 256 + s4l;
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) s4 += __shfl_xor_sync(0xffffffffu, s4, o);
+        long long s4s[1] = {(long long)s4h * 256 + s4l}, &s4 = s4s[0];
+        lanes_all<L>(s3s, red, Sum());
+        lanes_all<L>(s4s, red, Sum());
         const f2 m1 = pk(-(float)rint(mean(4.0 * (double)s3)));
         const f2 m2 = pk((float)mean((double)s4) * 6.103515625e-05f);  // 2^-14
         const f2 RN = pk(R * (float)p.N), four = pk(4.0f), one = pk(-1.0f);
@@ -736,7 +766,10 @@ int fill(NormArgs &a, const ict_tensor *X, const ict_tensor *gamma, const ict_te
 
 // Lanes per row: the fewest (a power of two from 4) whose lanes hold at most three vectors
 // each, so that the per-row work (reductions, root) is shared by as many values as possible
-// while a warp keeps enough loads in flight.
+// while a warp keeps enough loads in flight.  Rows above 1536 values take several warps: with
+// 4, 8 and 16 vectors a lane of one warp, rows of 2560, 4096 and 8192 values (30.7, 36.9 and 38.5
+// million) cost 47, 48 and 91 us forward and 105, 122 and 318 us backward, registers spilled,
+// against 41, 48 and 59 us forward and 67, 71 and 84 us with several warps.
 template <typename F>
 void dispatch(int nvec, F &&f) {
     auto go = [&](auto lanes) {
@@ -750,14 +783,14 @@ void dispatch(int nvec, F &&f) {
     else if (nvec <= 24) go(std::integral_constant<int, 8>());
     else if (nvec <= 48) go(std::integral_constant<int, 16>());
     else if (nvec <= 96) go(std::integral_constant<int, 32>());
-    else if (nvec <= 128) f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
-    else if (nvec <= 256) f(std::integral_constant<int, 32>(), std::integral_constant<int, 8>());
-    else f(std::integral_constant<int, 32>(), std::integral_constant<int, 16>());
+    else if (nvec <= 192) go(std::integral_constant<int, 64>());
+    else if (nvec <= 384) go(std::integral_constant<int, 128>());
+    else go(std::integral_constant<int, 256>());
 }
 
 template <int L>
 void finish_plan(NormArgs &a) {
-    a.fast = (a.gvo & (a.gvo - 1)) == 0 && a.gvo <= L && a.nvec % a.gvo == 0;
+    a.fast = (a.gvo & (a.gvo - 1)) == 0 && a.gvo <= (L < 32 ? L : 32) && a.nvec % a.gvo == 0;
     a.gso = a.fast ? __builtin_ctz((unsigned)a.gvo) : 0;
 }
 
