@@ -518,6 +518,9 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
         (st = check_out(dQ, rq, d->q_col, wq, a.D)) || (st = check_out(dK, rk, d->k_col, wk, a.D)) ||
         (st = check_out(dV, rk, d->v_col, wk, a.D)))
         return st;
+    if (host::share_columns(dQ, d->q_col, wq, dK, d->k_col, wk) || host::share_columns(dQ, d->q_col, wq, dV, d->v_col, wk) ||
+        host::share_columns(dK, d->k_col, wk, dV, d->v_col, wk))
+        return ICT_ERR_INVALID_ARG;
     if ((st = host::device_info(nullptr))) return st;
     uint8_t *base = (uint8_t *)ws;
     operand(a.op[OPD], dO, 0, a.Hq, a.Lq, lens_q, (int8_t *)(base + w.copy[OPD]));

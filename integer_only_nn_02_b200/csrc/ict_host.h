@@ -20,6 +20,14 @@ int check_tensor(const ict_tensor *t);
 int check_vec(const ict_tensor *t);  // 16-byte vectors: pointer, ld, cols, group width
 int tmap_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
             uint32_t box_outer, CUtensorMapSwizzle sw);
+// columns [ca, ca + wa) of a and [cb, cb + wb) of b share memory (tensors that start apart by less
+// than a row of the same length are taken as columns of one)
+inline bool share_columns(const ict_tensor *a, int64_t ca, int64_t wa, const ict_tensor *b, int64_t cb, int64_t wb) {
+    if (a->rows == 0 || b->rows == 0) return false;
+    const int64_t d = (int64_t)((intptr_t)b->mant - (intptr_t)a->mant);
+    if (a->ld == b->ld && d < a->ld && d > -a->ld) return d + cb < ca + wa && ca < d + cb + wb;
+    return d == 0;
+}
 void wait_limits(uint64_t *wait_ns, uint64_t *drain_ns);
 
 // Dynamic shared memory of a kernel, set once per device (the call costs a microsecond of every launch).

@@ -871,6 +871,10 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
     if (dbeta && (st = check_rows(dbeta, 1, X->cols))) return st;
     if (X->rows > (1 << 30)) return ICT_ERR_LAYOUT;
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < ict_layernorm_bwd_workspace(X)) return ICT_ERR_WORKSPACE;
+    // X and dY are read again after dX is written
+    if (host::share_columns(dX, 0, X->cols, X, 0, X->cols) || host::share_columns(dX, 0, X->cols, dY, 0, X->cols) ||
+        (dbeta && host::share_columns(dgamma, 0, X->cols, dbeta, 0, X->cols)))
+        return ICT_ERR_INVALID_ARG;
     if ((st = host::device_info(nullptr))) return st;
     cudaStream_t s = (cudaStream_t)stream;
     int64_t *acc = (int64_t *)ws;

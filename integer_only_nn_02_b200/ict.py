@@ -672,18 +672,22 @@ def attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, g_cols=32, lens_q=None,
 
 def attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, O: DevCE, dO: DevCE, stats: torch.Tensor, g_cols=32,
                   lens_q=None, lens_k=None, stream=None):
-    """(dQ, dK, dV) in (1, g_cols) groups, laid out like Q, K and V: operands that share one tensor share their
-    gradient's tensor (columns of no head stay unwritten)."""
-    made = {}
+    """(dQ, dK, dV) in (1, g_cols) groups, laid out like Q, K and V: operands that are different columns of one
+    tensor share their gradient's tensor (columns of no head stay unwritten)."""
+    made = []  # (operand, gradient, first columns and ends taken)
 
-    def like(t: DevCE) -> DevCE:
-        if id(t) not in made:
-            made[id(t)] = DevCE.near(t.mant, t.rows, t.cols, g_cols)
-        return made[id(t)]
+    def like(t: DevCE, first: int, heads: int) -> DevCE:
+        end = first + heads * c.head_dim
+        for t0, out, taken in made:
+            if t0 is t and all(end <= a or b <= first for a, b in taken):
+                taken.append((first, end))
+                return out
+        made.append((t, DevCE.near(t.mant, t.rows, t.cols, g_cols), [(first, end)]))
+        return made[-1][1]
 
     c = attn_desc(d)
     with _on(stream):
-        dQ, dK, dV = like(Q), like(K), like(V)
+        dQ, dK, dV = like(Q, c.q_col, c.heads_q), like(K, c.k_col, c.heads_kv), like(V, c.v_col, c.heads_kv)
         ict_attention_bwd(c, Q, K, V, lens_q, lens_k, O, dO, stats, dQ, dK, dV,
                           Q.mant.new_empty(ict_attention_workspace(True, c)))
     return dQ, dK, dV

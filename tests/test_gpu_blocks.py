@@ -310,6 +310,32 @@ def test_few_long_key_blocks_replayed(ict):
     status_ok(ict)
 
 
+def test_one_tensor_for_everything(ict):
+    """Q, K and V the same columns of one tensor: each has a gradient of its own."""
+    c = Case(2, 2, 2, 2, 33, 33, 64, G=32)
+    c.K = c.V = c.Q
+    got = c.gpu(ict, 32)
+    assert len({t.mant.data_ptr() for t in got[2:]}) == 3
+    c.check(ict, 32)
+
+
+@pytest.mark.parametrize("B,Lq,Lk", [(0, 5, 5), (2, 0, 7), (2, 7, 0), (1, 0, 0)])
+def test_nothing_to_attend(ict, B, Lq, Lk):
+    """No sequence, no query, no key: empty outputs, or zeros."""
+    D, H = 64, 2
+    make = lambda rows: ict.DevCE(torch.ones((rows, H * D), dtype=torch.int8, device="cuda"),  # noqa: E731
+                                  torch.zeros((rows, H * D // 32), dtype=torch.int8, device="cuda"), 1, 32)
+    d = dict(batch=B, heads_q=H, heads_kv=H, len_q=Lq, len_k=Lk, head_dim=D, causal=False, scale=SCALE[D])
+    q, k = make(B * Lq), make(B * Lk)
+    o, stats = ict.attention_fwd(d, q, k, k, 32)
+    dq, dk, dv = ict.attention_bwd(d, q, k, k, o, make(B * Lq), stats, 32)
+    torch.cuda.synchronize()
+    assert not stats.any()
+    for t, rows in ((o, B * Lq), (dq, B * Lq), (dk, B * Lk), (dv, B * Lk)):
+        assert t.mant.shape[0] == rows and not t.mant.any() and (t.exp == E_ZERO).all()
+    status_ok(ict)
+
+
 def test_lengths_outside_the_range(ict):
     """Lengths are clamped to [0, len]."""
     c = Case(6, 3, 2, 2, 40, 50, 64, True, [40, 1000, -3], [-1, 50, 2000])

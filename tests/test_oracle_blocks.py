@@ -260,6 +260,30 @@ def test_layernorm_and_values_refuse(ict):
     assert vals(out=(1 << 20) + 1) == ALIGN and vals(bf=0, out=(1 << 20) + 2) == ALIGN
 
 
+def test_gradients_that_share_memory_are_refused(ict):
+    T = lambda mant, rows=16, cols=256, **k: tensor(ict, rows, cols, mant=mant << 20, **k)  # noqa: E731
+    d = desc(ict, len_k=8)
+    o = T(3)
+
+    def back(dq, dk, dv, **kw):
+        c = ict.attn_desc(dict(d, **kw))
+        return ict.lib.ict_attention_bwd(c, T(1, cols=512), T(2, cols=512), T(2, cols=512), None, None, o, o, 1 << 20, dq, dk, dv,
+                                         1 << 20, 1 << 30, None)
+
+    w = T(7, cols=512)
+    assert back(T(4), T(5, cols=128), T(5, cols=128)) == INVALID
+    assert back(w, w, w) == INVALID and back(w, w, w, k_col=256, v_col=256) == INVALID
+    assert back(w, w, w, k_col=224, v_col=384) == INVALID
+    # a view that begins inside a row of the other tensor
+    inside = tensor(ict, 16, 128, mant=(7 << 20) + 128, ld=512)
+    assert back(w, inside, T(5, cols=128)) == INVALID and back(T(4), inside, w, v_col=128) == INVALID
+    L, v = ict.lib, tensor(ict, 1, 192, mant=9 << 20)
+    x, dy, dx, g = (T(m, 8, 192) for m in (1, 2, 3, 4))
+    db = tensor(ict, 1, 192, mant=10 << 20)
+    bwd = lambda dx, dg, db: L.ict_layernorm_bwd(x, v, dy, 1, 20, dx, dg, db, 1 << 20, 1 << 30, None)  # noqa: E731
+    assert bwd(x, v, db) == INVALID and bwd(dy, v, db) == INVALID and bwd(dx, db, db) == INVALID
+
+
 def test_other_mantissa_widths_are_refused(ict):
     ict.ict_set_mantissa_bits(6)
     try:
