@@ -177,7 +177,10 @@ class DevCE:
         host less than naming the device)."""
         g_cols = max(1, min(g_cols, cols)) if cols else max(1, g_cols)
         ld = -(-cols // 16) * 16 if cols else 16
-        return DevCE(t.new_empty((rows, ld)), t.new_empty((rows, cdiv(cols, g_cols))), 1, g_cols, cols=cols)
+        new = DevCE.__new__(DevCE)  # nothing to check
+        new.mant, new.exp = t.new_empty((rows, ld)), t.new_empty((rows, -(-cols // g_cols)))
+        new.rows, new.cols, new.ld, new.g_rows, new.g_cols = rows, cols, ld, 1, g_cols
+        return new
 
     @staticmethod
     def from_host(t: CE, device="cuda", pin=False):
@@ -425,13 +428,20 @@ def ict_softmax_ce(Z: DevCE, target: torch.Tensor, loss: torch.Tensor, dZ: DevCE
            "ict_softmax_ce")
 
 
+_byref = ctypes.byref
+
+
 def _refs(*tensors: DevCE | None):
     """The tensors as arguments of one library call, which runs on the current device."""
     cur, refs = torch._C._cuda_getDevice(), []
     for t in tensors:
-        if t is not None and t.mant.get_device() != cur:
-            raise ValueError(f"tensor on {t.mant.device}, but the current device is cuda:{cur}")
-        refs.append(ctypes.byref(t.c()) if t is not None else None)
+        if t is None:
+            refs.append(None)
+            continue
+        m = t.mant
+        if m.get_device() != cur:
+            raise ValueError(f"tensor on {m.device}, but the current device is cuda:{cur}")
+        refs.append(_byref(ict_tensor(m.data_ptr(), t.exp.data_ptr(), t.rows, t.cols, t.ld, t.g_rows, t.g_cols)))
     return refs
 
 
@@ -639,9 +649,12 @@ def softmax_ce(Z: DevCE, target: torch.Tensor, g_cols: int | None = None, stream
     return loss, dZ
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocations made inside belong to the stream that the call runs on."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return torch.cuda.stream(stream) if stream is not None else _HERE
 
 
 def layernorm_fwd(X: DevCE, gamma: DevCE, beta: DevCE | None = None, eps=(1, 20), g_cols=32, stream=None) -> DevCE:
@@ -697,8 +710,8 @@ def values(t: DevCE, dtype=torch.bfloat16, stream=None) -> torch.Tensor:
     """The values C 2^e of t [rows, cols]."""
     with _on(stream):
         out = t.mant.new_empty((t.rows, t.cols), dtype=dtype)
-        (r,) = _refs(t)
-        _check(lib.ict_values(r, _VALUE_TYPES[dtype], out.data_ptr(), max(t.cols, 1), _stream()), "ict_values")
+        code = lib.ict_values(_refs(t)[0], _VALUE_TYPES[dtype], out.data_ptr(), max(t.cols, 1), _stream())
+    _check(code, "ict_values")
     return out
 
 
