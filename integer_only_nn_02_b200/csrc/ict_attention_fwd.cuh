@@ -565,10 +565,13 @@ __global__ void __launch_bounds__(FwdCfg<DP>::kThreads, DP == 64 ? 2 : 1)
             // the output's columns are free
             if (ok && on > 0 && !(DP == 64 && w.nt > 1)) ok = wait(bar_oe, on - 1);
             for (int u = 0; u < nu && ok; ++u) {
+                // one product is open at a time, the last two of an item included: of two open phases a parity
+                // cannot tell the first from the second, and the next item's scores would be issued into
+                // weights that a product still reads
+                if (u > 0 && !(ok = wait(bar_ee, pn - 1))) break;
                 if (u + 1 < nu) {  // the next scores, in the buffer of the weights u - 1
-                    if (u > 0) ok = wait(bar_ee, pn - 1);
                     // before its barrier completes another phase, every warp has seen pass 1's last
-                    else if (w.nt > 1) ok = wait(bar_se + 8, (rd_par >> 1 ^ 1) & 1);
+                    if (u == 0 && w.nt > 1) ok = wait(bar_se + 8, (rd_par >> 1 ^ 1) & 1);
                     const int half = (u + 1) % PER;
                     if (!ok || !(ok = scores(nTN, (u + 1) & 1, ((u + 1) & 1) * L::TN, half, half == PER - 1 || u + 2 == nu,
                                              u + 2 == nu)))

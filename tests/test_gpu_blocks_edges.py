@@ -1,0 +1,36 @@
+"""Attention and layer norm at the edges of their ranges: persistent blocks with many items, exponents at the ends,
+rows of almost nothing, tensors that hold more than the heads."""
+import numpy as np
+import pytest
+import torch
+
+from integer_only_nn_02_b200.workloads import CE, E_ZERO
+from oracle import blocks
+from tests.test_gpu_blocks import Case, _operators, same, status_ok
+from tests.test_oracle_pins import rand_ce
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ict():
+    from integer_only_nn_02_b200 import ict as _ict
+
+    return _ict
+
+
+@pytest.mark.parametrize("D,L,causal,ragged", [(64, 129, False, False), (64, 200, True, True), (64, 320, False, True),
+                                               (64, 500, True, False), (128, 129, False, True), (128, 300, True, False),
+                                               (96, 512, False, False)])
+def test_many_items_of_several_steps(ict, D, L, causal, ragged):
+    """Up to 512 keys a block walks through many items, the next one's scores in the columns of the last one's
+    weights: every item's output, call after call, is the plain form's."""
+    m = _operators()
+    st = m.prepare(dict(op="attn_fwd", B=30, Hq=12, Hkv=12, Lq=L, Lk=L, D=D, causal=causal, ragged=ragged, packed=True, G=32), L)
+    m.own = False
+    ref = m.run(st)
+    m.own = True
+    for _ in range(8):
+        for x, y in zip(m.run(st), ref):
+            assert torch.equal(x, y)
+    status_ok(ict)
