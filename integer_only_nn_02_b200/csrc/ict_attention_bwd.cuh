@@ -102,8 +102,8 @@ struct DqCfg {
     static constexpr int NB = DP == 64 ? 3 : 2;               // score buffers (128 columns each)
     static constexpr int kAcc = DP == 64 ? 384 : 256;         // dQ's column
     static constexpr int kOffK = QS * 2 * kTile, kOffV = kOffK + KS * kTile;  // Q stage: Q tile, dO tile
-    static constexpr int kOffRed = kOffV + VS * kTile;  // [2][8][128] float2, [2][4][128] int
-    static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8 + 2 * 4 * 128 * 4;
+    static constexpr int kOffRed = kOffV + VS * kTile;  // [2][8][128] float2, [4][4][128] int
+    static constexpr int kOffBar = kOffRed + 2 * 8 * 128 * 8 + 4 * 4 * 128 * 4;
     static constexpr int kBars = 2 * (QS + KS + VS) + 3 * NB + 4;
     static constexpr int kBytes = kOffBar + kBars * 8 + 16 + 1024;
     static constexpr int kThreads = 32 * kSoftWarps + 64;
@@ -337,7 +337,9 @@ __global__ void __launch_bounds__(DqCfg<DP>::kThreads, 1)
             }
             // the item's output is this turn's pair's; the other leaves its maxima and goes on
             const int turn = on & 1;
-            int *red = (int *)(smem + L::kOffRed + 2 * 8 * 128 * 8) + turn * 4 * 128;
+            // four of these in turn: a warp may still read this output's maxima when another leaves those of the
+            // output after the next, but not once both have met again at that one's barrier
+            int *red = (int *)(smem + L::kOffRed + 2 * 8 * 128 * 8) + (on & 3) * 4 * 128;
             red[wg * 128 + et] = max(tmax - 0x4B400000, 0x4B400000 - tmin);
             if (pair != turn) {
                 named_bar_arrive(3 + turn, NS);

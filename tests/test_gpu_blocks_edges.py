@@ -34,3 +34,19 @@ def test_many_items_of_several_steps(ict, D, L, causal, ragged):
         for x, y in zip(m.run(st), ref):
             assert torch.equal(x, y)
     status_ok(ict)
+
+
+@pytest.mark.parametrize("D,G", [(64, 32), (64, 16), (128, 128)])
+def test_backward_items_of_one_and_two_steps(ict, D, G):
+    """Sequences of 1 to 128 keys: pairs of warpgroups run ahead of each other by whole items."""
+    m = _operators()
+    lens = torch.tensor([1, 128, 64, 65, 3, 90, 128, 20, 0, 70] * 4, dtype=torch.int32, device="cuda")
+    m._lens = lambda g, B, L, ragged: lens
+    st = m.prepare(dict(op="attn_bwd", B=40, Hq=12, Hkv=12, Lq=128, Lk=128, D=D, causal=False, ragged=True, packed=True, G=G), D)
+    m.own = False
+    ref = m.run(st)
+    m.own = True
+    for _ in range(8):
+        for x, y in zip(m.run(st), ref):
+            assert torch.equal(x, y)
+    status_ok(ict)
