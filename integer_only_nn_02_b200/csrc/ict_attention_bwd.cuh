@@ -516,6 +516,7 @@ __device__ __noinline__ bool join_parts(const AccCols acc, int c0, uint4 *sums, 
         for (int q = 0; q < 4; ++q) tmem_st4(acc.hi + (z >> 1) * acc.lo + c0 + (z & 1) * 16 + 4 * q, t[q]);
     }
     tmem_st_wait();
+    tc_fence_before();  // other warpgroups may read these columns (AccCols::exact) behind their next barrier
     return true;
 }
 

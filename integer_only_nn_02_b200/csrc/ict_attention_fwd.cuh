@@ -343,6 +343,7 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
         gmax[(c0 / 16 + s) * stride] = make_float2(m, w);
     }
     named_bar_sync(bar, nthreads);
+    tc_fence_after();  // group_fit reads the other warpgroups' columns, which join_parts may have written
     GroupFit f{kEZero, 0.0f, 0.5f};
 #pragma unroll 1
     for (int s = 0; s < SEGS; ++s) {

@@ -50,3 +50,18 @@ def test_backward_items_of_one_and_two_steps(ict, D, G):
         for x, y in zip(m.run(st), ref):
             assert torch.equal(x, y)
     status_ok(ict)
+
+
+@pytest.mark.parametrize("D,G,Lq", [(64, 64, 1500), (128, 128, 1200), (112, 112, 900)])
+def test_joined_parts_with_wide_groups(ict, D, G, Lq):
+    """More than 1024 queries on a key block, shared by several thread blocks, in groups as wide as a head: the last
+    part's sums are written to and read from the accumulators by different warpgroups."""
+    m = _operators()
+    st = m.prepare(dict(op="attn_bwd", B=1, Hq=4, Hkv=2, Lq=Lq, Lk=300, D=D, causal=False, ragged=False, packed=False, G=G), D)
+    m.own = False
+    ref = m.run(st)
+    m.own = True
+    for _ in range(4):
+        for x, y in zip(m.run(st), ref):
+            assert torch.equal(x, y)
+    status_ok(ict)
