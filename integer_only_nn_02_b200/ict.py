@@ -156,6 +156,8 @@ class DevCE:
 
     def __init__(self, mant: torch.Tensor, exp: torch.Tensor, g_rows: int, g_cols: int, cols=None):
         assert mant.dtype == torch.int8 and exp.dtype == torch.int8 and mant.is_cuda
+        if exp.device != mant.device:  # the kernels read both
+            raise ValueError(f"mantissas on {mant.device}, exponents on {exp.device}")
         self.mant, self.exp = mant, exp
         self.rows = int(mant.shape[0])
         self.cols = int(cols if cols is not None else mant.shape[1])
@@ -438,10 +440,10 @@ def _refs(*tensors: DevCE | None):
         if t is None:
             refs.append(None)
             continue
-        m = t.mant
-        if m.get_device() != cur:
-            raise ValueError(f"tensor on {m.device}, but the current device is cuda:{cur}")
-        refs.append(_byref(ict_tensor(m.data_ptr(), t.exp.data_ptr(), t.rows, t.cols, t.ld, t.g_rows, t.g_cols)))
+        m, e = t.mant, t.exp
+        if m.get_device() != cur or e.get_device() != cur:
+            raise ValueError(f"mantissas on {m.device}, exponents on {e.device}, but the current device is cuda:{cur}")
+        refs.append(_byref(ict_tensor(m.data_ptr(), e.data_ptr(), t.rows, t.cols, t.ld, t.g_rows, t.g_cols)))
     return refs
 
 
