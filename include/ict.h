@@ -418,7 +418,8 @@ int32_t ict_softmax_ce(const ict_tensor *Z, const int32_t *target, int32_t *loss
 /*   dX = FIT(rn24(t rn24(R N)));  dgamma = FIT(sum over rows of A(dY) h 2^-8) and          */
 /*   dbeta = FIT(sum over rows of A(dY)), A here per column group over the rows, the sums   */
 /*   exact.  dbeta may be NULL.  h is recomputed from X: no statistics are kept.  dX may    */
-/*   not share memory with X or dY, nor dgamma with dbeta (ICT_ERR_INVALID_ARG).            */
+/*   not share mantissas or exponents with X or dY, nor the gradients with each other        */
+/*   (ICT_ERR_INVALID_ARG).                                                                  */
 /* X, dY, Y, dX: [rows][N], row-local groups of any widths; gamma, beta, dgamma, dbeta:     */
 /* [1][N].  N and all group widths (below N) multiples of 16, N <= 8192 (ICT_ERR_LAYOUT);   */
 /* pointers and ld 16-byte aligned.  0 <= eps_mul <= 512, 0 <= eps_shift <= 64.             */
@@ -460,8 +461,9 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
 /* len_k <= 65536, backward also len_q heads_q / heads_kv <= 65536 (ICT_ERR_LAYOUT); columns,    */
 /* widths and group widths multiples of 16, row-local groups; an output's groups lie inside      */
 /* one head (head_dim and the first column multiples of the group width).  stats 8-byte          */
-/* aligned.  1 <= scale_mul <= 512, 0 <= scale_shift <= 64.  The columns of dQ, dK and dV may    */
-/* not share memory (ICT_ERR_INVALID_ARG), also where Q, K and V are the same columns.          */
+/* aligned.  1 <= scale_mul <= 512, 0 <= scale_shift <= 64.  The heads' columns of dQ, dK and dV */
+/* may not share mantissas or exponents (ICT_ERR_INVALID_ARG), also where Q, K and V are the    */
+/* same columns; rows of different ld in one range of memory count as shared.                   */
 typedef struct {
     int32_t batch, heads_q, heads_kv, len_q, len_k, head_dim, causal, scale_mul, scale_shift;
     int32_t q_col, k_col, v_col;

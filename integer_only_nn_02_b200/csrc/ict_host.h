@@ -20,13 +20,29 @@ int check_tensor(const ict_tensor *t);
 int check_vec(const ict_tensor *t);  // 16-byte vectors: pointer, ld, cols, group width
 int tmap_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
             uint32_t box_outer, CUtensorMapSwizzle sw);
-// columns [ca, ca + wa) of a and [cb, cb + wb) of b share memory (tensors that start apart by less
-// than a row of the same length are taken as columns of one)
+// columns [c, c + w) of `rows` rows of bytes, ld apart
+struct Bytes {
+    intptr_t at;
+    int64_t rows, ld, w;
+};
+inline Bytes mantissas(const ict_tensor *t, int64_t c, int64_t w) { return {(intptr_t)t->mant + c, t->rows, t->ld, w}; }
+inline Bytes exponents(const ict_tensor *t, int64_t c, int64_t w) {
+    const int64_t g0 = c / t->g_cols, g1 = (c + w + t->g_cols - 1) / t->g_cols;
+    return {(intptr_t)t->exp + g0, (t->rows + t->g_rows - 1) / t->g_rows, (t->cols + t->g_cols - 1) / t->g_cols, g1 - g0};
+}
+// a and b share a byte.  Rows of one ld repeat the pattern of the first two; rows of different ld whose ranges
+// meet count as shared.
+inline bool meet(const Bytes &a, const Bytes &b) {
+    if (a.at > b.at) return meet(b, a);
+    if (a.rows == 0 || b.rows == 0 || a.w == 0 || b.w == 0) return false;
+    const int64_t d = b.at - a.at;
+    if (d >= (a.rows - 1) * a.ld + a.w) return false;
+    return a.ld != b.ld || d % a.ld < a.w || d % a.ld + b.w > a.ld;
+}
+// columns [ca, ca + wa) of a and [cb, cb + wb) of b share memory, mantissas or exponents
 inline bool share_columns(const ict_tensor *a, int64_t ca, int64_t wa, const ict_tensor *b, int64_t cb, int64_t wb) {
-    if (a->rows == 0 || b->rows == 0) return false;
-    const int64_t d = (int64_t)((intptr_t)b->mant - (intptr_t)a->mant);
-    if (a->ld == b->ld && d < a->ld && d > -a->ld) return d + cb < ca + wa && ca < d + cb + wb;
-    return d == 0;
+    const Bytes x[2] = {mantissas(a, ca, wa), exponents(a, ca, wa)}, y[2] = {mantissas(b, cb, wb), exponents(b, cb, wb)};
+    return meet(x[0], y[0]) || meet(x[0], y[1]) || meet(x[1], y[0]) || meet(x[1], y[1]);
 }
 void wait_limits(uint64_t *wait_ns, uint64_t *drain_ns);
 

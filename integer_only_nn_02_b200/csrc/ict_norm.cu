@@ -872,9 +872,8 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
     if (X->rows > (1 << 30)) return ICT_ERR_LAYOUT;
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < ict_layernorm_bwd_workspace(X)) return ICT_ERR_WORKSPACE;
     // X and dY are read again after dX is written
-    if (host::share_columns(dX, 0, X->cols, X, 0, X->cols) || host::share_columns(dX, 0, X->cols, dY, 0, X->cols) ||
-        (dbeta && host::share_columns(dgamma, 0, X->cols, dbeta, 0, X->cols)))
-        return ICT_ERR_INVALID_ARG;
+    auto share = [&](const ict_tensor *t, const ict_tensor *u) { return t && u && host::share_columns(t, 0, X->cols, u, 0, X->cols); };
+    if (share(dX, X) || share(dX, dY) || share(dX, dgamma) || share(dX, dbeta) || share(dgamma, dbeta)) return ICT_ERR_INVALID_ARG;
     if ((st = host::device_info(nullptr))) return st;
     cudaStream_t s = (cudaStream_t)stream;
     int64_t *acc = (int64_t *)ws;
