@@ -804,7 +804,7 @@ int run_rows(const NormArgs &a, int lanes, size_t smem, cudaStream_t s) {
     uint64_t f = fits[dev].load(std::memory_order_relaxed);
     if (f >> 16 != smem || f == 0) {
         int per = 0;
-        if (smem > 48 * 1024 && (st = host::allow_smem<Kernel>((int)smem))) return st;
+        if ((st = host::allow_smem<Kernel>((int)smem))) return st;  // (the kernel's static memory counts towards 48 KB too)
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, 256, smem) != cudaSuccess || per < 1) return ICT_ERR_CUDA;
         f = (uint64_t)smem << 16 | (uint64_t)per;
         fits[dev].store(f, std::memory_order_relaxed);

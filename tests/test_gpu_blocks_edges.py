@@ -65,3 +65,16 @@ def test_joined_parts_with_wide_groups(ict, D, G, Lq):
         for x, y in zip(m.run(st), ref):
             assert torch.equal(x, y)
     status_ok(ict)
+
+
+@pytest.mark.parametrize("N,g_out", [(6112, 16), (6128, 6128), (6144, 64), (6144, 48), (6016, 32), (6160, 16)])
+def test_layernorm_rows_near_48_kb(ict, N, g_out):
+    """Rows whose weight and bias as floats take almost the 48 KB of shared memory that a kernel has without asking."""
+    rng = np.random.default_rng(N + g_out)
+    X, dY = (rand_ce(rng, 3, N, 1, 16, elo=e, ehi=e + 2) for e in (-6, -16))
+    gamma, beta = rand_ce(rng, 1, N, 1, 16, elo=-7, ehi=-6), rand_ce(rng, 1, N, 1, 16, elo=-9, ehi=-6)
+    x, dy, g, b = (ict.DevCE.from_host(t) for t in (X, dY, gamma, beta))
+    same(ict.layernorm_fwd(x, g, b, (1, 20), g_out).to_host(), blocks.layernorm_fwd(X, gamma, beta, (1, 20), g_out), "Y")
+    for t, r in zip(ict.layernorm_bwd(x, g, dy, (1, 20), g_out), blocks.layernorm_bwd(X, gamma, dY, (1, 20), g_out)):
+        same(t.to_host(), r)
+    status_ok(ict)
