@@ -380,7 +380,7 @@ int launch_fwd(const AttnArgs &a, cudaStream_t s) {
     CUtensorMap q, k, v;
     int st;
     if ((st = copy_map(&q, a, OPQ)) || (st = copy_map(&k, a, OPK)) || (st = copy_map(&v, a, OPV))) return st;
-    if ((st = host::allow_smem<attn_fwd_kernel<DP>>(L::kBytes))) return st;
+    if ((st = host::allow_smem<attn_fwd_kernel<DP>, L::kBytes>())) return st;
     AttnLimits lim;
     host::wait_limits(&lim.wait_ns, &lim.drain_ns);
     const int64_t items = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
@@ -433,7 +433,7 @@ int launch_bwd(const AttnArgs &a, cudaStream_t s) {
         using L = DqCfg<DP>;
         constexpr int NL = DP / 16;
         attn_row_kernel<NL><<<(unsigned)host::cdiv(rows, 256 / NL), 256, 0, s>>>(a);
-        if ((st = host::allow_smem<attn_dq_kernel<DP>>(L::kBytes))) return st;
+        if ((st = host::allow_smem<attn_dq_kernel<DP>, L::kBytes>())) return st;
         const int64_t items = host::cdiv(a.Lq, kQTile) * a.B * a.Hq;
         attn_dq_kernel<DP><<<blocks_for(items, 1, a.Lk), L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
         host::counted(2);
@@ -449,11 +449,12 @@ int launch_bwd(const AttnArgs &a, cudaStream_t s) {
             if (cudaMemsetAsync(a.tickets, 0, (size_t)a.blocks * (DP / 64) * 4, s) != cudaSuccess) return ICT_ERR_CUDA;
         }
         if constexpr (DP == 64) {
-            if ((st = host::allow_smem<attn_dkv_kernel<64, 3>>(L::kBytes))) return st;
+            if ((st = host::allow_smem<attn_dkv_kernel<64, 3>, L::kBytes>())) return st;
             attn_dkv_kernel<64, 3><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
             host::counted(1);
         } else {
-            if ((st = host::allow_smem<attn_dkv_kernel<DP, 1>>(L::kBytes)) || (st = host::allow_smem<attn_dkv_kernel<DP, 2>>(L::kBytes))) return st;
+            if ((st = host::allow_smem<attn_dkv_kernel<DP, 1>, L::kBytes>()) || (st = host::allow_smem<attn_dkv_kernel<DP, 2>, L::kBytes>()))
+                return st;
             attn_dkv_kernel<DP, 2><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
             attn_dkv_kernel<DP, 1><<<blocks, L::kThreads, L::kBytes, s>>>(q, k, v, d, a, lim, (int)items);
             host::counted(2);

@@ -46,15 +46,16 @@ inline bool share_columns(const ict_tensor *a, int64_t ca, int64_t wa, const ict
 }
 void wait_limits(uint64_t *wait_ns, uint64_t *drain_ns);
 
-// Dynamic shared memory of a kernel, set once per device (the call costs a microsecond of every launch).
-template <auto Kernel>
-int allow_smem(int bytes) {
-    static std::atomic<int> set[64];
+// Dynamic shared memory of a kernel, set once per device (the call costs a microsecond of every launch).  The size is
+// the kernel's largest, whatever a call needs: threads that meet here set the same value, and it never goes down.
+template <auto Kernel, int Bytes>
+int allow_smem() {
+    static std::atomic<bool> set[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return ICT_ERR_CUDA;
-    if (set[dev].load(std::memory_order_acquire) >= bytes) return ICT_OK;
-    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return ICT_ERR_CUDA;
-    set[dev].store(bytes, std::memory_order_release);
+    if (set[dev].load(std::memory_order_acquire)) return ICT_OK;
+    if (cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Bytes) != cudaSuccess) return ICT_ERR_CUDA;
+    set[dev].store(true, std::memory_order_release);
     return ICT_OK;
 }
 

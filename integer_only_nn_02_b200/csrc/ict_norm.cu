@@ -794,6 +794,9 @@ void finish_plan(NormArgs &a) {
     a.gso = a.fast ? __builtin_ctz((unsigned)a.gvo) : 0;
 }
 
+// Two floats a column, and the maxima of the output groups of a block's rows: 256 / L rows of at most 3 L groups.
+constexpr int kMaxSmem = kMaxCols * 8 + 256 * 3 * 4;
+
 template <auto Kernel>
 int run_rows(const NormArgs &a, int lanes, size_t smem, cudaStream_t s) {
     static std::atomic<uint64_t> fits[64];  // per device: shared memory asked for last, and how many blocks fit
@@ -804,7 +807,8 @@ int run_rows(const NormArgs &a, int lanes, size_t smem, cudaStream_t s) {
     uint64_t f = fits[dev].load(std::memory_order_relaxed);
     if (f >> 16 != smem || f == 0) {
         int per = 0;
-        if ((st = host::allow_smem<Kernel>((int)smem))) return st;  // (the kernel's static memory counts towards 48 KB too)
+        // (asked for at any size: the kernel's static memory counts towards the 48 KB that need no asking)
+        if ((st = host::allow_smem<Kernel, kMaxSmem>())) return st;
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, Kernel, 256, smem) != cudaSuccess || per < 1) return ICT_ERR_CUDA;
         f = (uint64_t)smem << 16 | (uint64_t)per;
         fits[dev].store(f, std::memory_order_relaxed);

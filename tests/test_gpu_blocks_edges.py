@@ -1,5 +1,9 @@
 """Attention and layer norm at the edges of their ranges: persistent blocks with many items, exponents at the ends,
 rows of almost nothing, tensors that hold more than the heads."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +14,7 @@ from tests.test_gpu_blocks import Case, _operators, same, status_ok
 from tests.test_oracle_pins import rand_ce
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -78,3 +83,38 @@ def test_layernorm_rows_near_48_kb(ict, N, g_out):
     for t, r in zip(ict.layernorm_bwd(x, g, dy, (1, 20), g_out), blocks.layernorm_bwd(X, gamma, dY, (1, 20), g_out)):
         same(t.to_host(), r)
     status_ok(ict)
+
+
+THREADS = """
+import sys, threading
+import numpy as np, torch
+from integer_only_nn_02_b200 import ict
+from integer_only_nn_02_b200.workloads import CE
+torch.cuda.init()
+widths = [8192, 6208, 7168, 8000, 6400, 8192, 6800, 7600]
+xs = []
+for k, n in enumerate(widths):
+    rng = np.random.default_rng(k)
+    make = lambda rows: ict.DevCE.from_host(CE(rng.integers(-127, 128, (rows, n), dtype=np.int8), np.zeros((rows, n // 16), np.int8), 1, 16))
+    xs.append((make(2), make(1), torch.cuda.Stream()))
+torch.cuda.synchronize()
+start, failed = threading.Barrier(len(widths)), []
+def work(x, g, s):
+    torch.cuda.set_device(0)
+    start.wait()
+    try:
+        for _ in range(20):
+            ict.layernorm_fwd(x, g, None, (1, 20), 32, stream=s)
+    except Exception as e:
+        failed.append(repr(e))
+ts = [threading.Thread(target=work, args=t) for t in xs]
+[t.start() for t in ts]; [t.join() for t in ts]
+torch.cuda.synchronize()
+sys.exit(f"{failed}" if failed else 0)
+"""
+
+
+def test_first_calls_of_several_threads(ict):
+    """The first calls of a process, from eight threads at once, with rows that need different amounts of shared memory."""
+    r = subprocess.run([sys.executable, "-c", THREADS], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
