@@ -57,7 +57,7 @@ def test_backward_items_of_one_and_two_steps(ict, D, G):
     status_ok(ict)
 
 
-@pytest.mark.parametrize("D,G,Lq", [(64, 64, 1500), (128, 128, 1200), (112, 112, 900)])
+@pytest.mark.parametrize("D,G,Lq", [(64, 64, 1500), (128, 128, 1200), (96, 96, 900)])
 def test_joined_parts_with_wide_groups(ict, D, G, Lq):
     """More than 1024 queries on a key block, shared by several thread blocks, in groups as wide as a head: the last
     part's sums are written to and read from the accumulators by different warpgroups."""
