@@ -179,5 +179,11 @@ __device__ __forceinline__ int quot_mant_fast(double n, double rden) {
     const double q = (n * rden + 768.0) - 768.0;
     return __double2loint(q + 6755399441055744.0);
 }
+// The same at a group exponent of 127, which may be the one that the group needs or capped: there quotients
+// above 127 saturate.
+__device__ __forceinline__ int quot_mant_capped(double n, double rden) {
+    const double q = fmin(fmax(n * rden, -128.0), 128.0);
+    return min(max(quot_mant_fast(q, 1.0), -127), 127);
+}
 
 }  // namespace ict

@@ -146,7 +146,7 @@ __device__ __forceinline__ void round16(const AccCols &acc, int col, const float
             todo &= todo - 1;
             const double x = acc.exact(col + q);
             if (near >> q & 1) {
-                const int y = capped ? (int)fmin(fmax(x * rden, -127.0), 127.0) : quot_mant_fast(x, rden);
+                const int y = capped ? quot_mant_capped(x, rden) : quot_mant_fast(x, rden);
                 const uint32_t sh = 8 * (q & 3), keep = ~(0xffu << sh), put = (uint32_t)(y & 0xff) << sh;
                 const int k = q >> 2;
                 w0 = k == 0 ? (w0 & keep) | put : w0;
@@ -173,7 +173,7 @@ __device__ __noinline__ uint4 exact_round16(const int *x, uint4 w, int e, float 
 #pragma unroll 1
     for (; near; near &= near - 1) {
         const int q = __ffs(near) - 1, k = q >> 2;
-        const int y = e == 127 ? (int)fmin(fmax(x[q] * rden, -127.0), 127.0) : quot_mant_fast(x[q], rden);
+        const int y = e == 127 ? quot_mant_capped(x[q], rden) : quot_mant_fast(x[q], rden);
         const uint32_t sh = 8 * (q & 3), keep = ~(0xffu << sh), put = (uint32_t)(y & 0xff) << sh;
         w.x = k == 0 ? (w.x & keep) | put : w.x;
         w.y = k == 1 ? (w.y & keep) | put : w.y;

@@ -118,3 +118,58 @@ def test_first_calls_of_several_threads(ict):
     """The first calls of a process, from eight threads at once, with rows that need different amounts of shared memory."""
     r = subprocess.run([sys.executable, "-c", THREADS], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("Lq,Lk,D,G,g_out", [(40, 150, 64, 32, 32), (3, 1100, 64, 64, 64), (1, 2000, 128, 32, 16), (140, 40, 128, 128, 128),
+                                             (5, 1500, 64, 16, 64), (2, 3, 16, 16, 16)])
+def test_attention_of_the_largest_values(ict, Lq, Lk, D, G, g_out):
+    """Values whose exponents are 126 and 127: the outputs need at most 127, and are rounded as any others, by the
+    kernels for tiles and for a few queries alike."""
+    c = Case(Lk + D, 2, 2, 1, Lq, Lk, D, G=G)
+    c.V = rand_ce(np.random.default_rng(D), 2 * Lk, D, 1, G, elo=126, ehi=127)
+    o, stats = blocks.attention_fwd(c.d, c.Q, c.K, c.V, *c.lens, g_out)
+    got = c.gpu(ict, g_out, back=False)
+    same(got[0].to_host(), o, "O")
+    if D == 16 or Lk == 40:
+        assert (o.exp == 127).any()
+    status_ok(ict)
+
+
+def test_attention_of_a_tie_at_the_largest_exponent(ict):
+    """The mean of 101 2^127 and 102 2^127 rounds to 102."""
+    D = 16
+    zero = CE(np.zeros((2, D), np.int8), np.full((2, 1), E_ZERO, np.int8), 1, D)
+    V = CE(np.repeat(np.array([[101], [102]], np.int8), D, 1), np.full((2, 1), 127, np.int8), 1, D)
+    V.mant[:, 1] = [-102, -101]
+    q, v = ict.DevCE.from_host(zero), ict.DevCE.from_host(V)
+    o, _ = ict.attention_fwd(dict(batch=1, heads_q=1, heads_kv=1, len_q=2, len_k=2, head_dim=D, scale=(1, 2)), q, q, v, D)
+    m = o.to_host().mant
+    assert (m[:, 0] == 102).all() and (m[:, 1] == -102).all() and (m[:, 2:] == 102).all() and (o.to_host().exp == 127).all()
+    status_ok(ict)
+
+
+@pytest.mark.parametrize("D,G,Lq,Lk", [(64, 32, 40, 150), (64, 64, 40, 150), (128, 32, 40, 150), (128, 128, 150, 40),
+                                       (64, 16, 1100, 30)])
+def test_attention_gradients_at_the_largest_exponent(ict, D, G, Lq, Lk):
+    """dO times 2^s makes every gradient times 2^s, rounded alike up to an exponent of 127 and saturated, with the
+    status raised, beyond it."""
+    c = Case(D + G, 1, 2, 1, Lq, Lk, D, G=G)
+    ref = [t.to_host() for t in c.gpu(ict, G)[2:]]
+    tops = [int(t.exp[t.exp != E_ZERO].max()) for t in ref]
+    base, hit = c.dO.exp.astype(int), 0
+    for s in [127 - t for t in tops] + [min(127 - int(base.max()), 140 - min(tops))]:
+        c.dO.exp = np.where(base == E_ZERO, base, base + s).astype(np.int8)
+        for name, t, r in zip(("dQ", "dK", "dV"), [t.to_host() for t in c.gpu(ict, G)[2:]], ref):
+            zero = r.exp == E_ZERO
+            k = np.where(zero, 0, r.exp.astype(int) + s - 127)  # how far the exponent passes 127
+            assert np.array_equal(t.exp, np.where(zero, E_ZERO, np.minimum(r.exp.astype(int) + s, 127))), (name, s)
+            kk = np.repeat(k, G, 1)
+            fits = kk <= 0
+            assert np.array_equal(t.mant[fits], r.mant[fits]), (name, s)
+            over = (np.abs(r.mant) - 0.5) * np.exp2(np.maximum(kk, 0)) >= 127.5
+            over &= ~fits
+            assert np.array_equal(t.mant[over], 127 * np.sign(r.mant[over])), (name, s)
+            hit += int((k == 0).any())
+        code, _ = ict.ict_get_device_status()
+        assert (code != 0) == (max(tops) + s > 127)
+    assert hit >= 3
