@@ -184,7 +184,8 @@ __device__ __forceinline__ uint4 fit16(const f2 (&y)[8], uint32_t top, int base,
     }
     const int need = need_rel_f32(top, 8) + base;
     e = finalize_exp(need);
-    const f2 sc = pk(pow2f(base - e)), mg = pk(kMagic);
+    // a capped exponent lies up to 250 below base; every y is 0 or at least 2^-26, so 2^127 saturates as well
+    const f2 sc = pk(pow2f(min(base - e, 127))), mg = pk(kMagic);
     uint32_t o[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {

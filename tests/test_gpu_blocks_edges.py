@@ -173,3 +173,27 @@ def test_attention_gradients_at_the_largest_exponent(ict, D, G, Lq, Lk):
         code, _ = ict.ict_get_device_status()
         assert (code != 0) == (max(tops) + s > 127)
     assert hit >= 3
+
+
+@pytest.mark.parametrize("G,g_out", [(32, 32), (16, 48), (96, 96)])
+def test_layernorm_gradients_beyond_the_largest_exponent(ict, G, g_out):
+    """dX scales with weight and dY: rounded alike up to an exponent of 127, and saturated with its sign beyond."""
+    rng = np.random.default_rng(G)
+    X, gamma, dY = (rand_ce(rng, r, 96, 1, G, elo=e, ehi=e) for r, e in ((6, -100), (1, -20), (6, -120)))
+    ref = blocks.layernorm_bwd(X, gamma, dY, (0, 0), g_out)[0]
+    top = int(ref.exp[ref.exp != E_ZERO].max())
+    x = ict.DevCE.from_host(X)
+    for s in [127 - top + k for k in (0, 1, 2, 7, 20, 100, 127, 128, 129, 130, 160, 200)]:
+        up = min(147, s)  # of the weight, the rest of dY
+        if s - up > 247:
+            continue
+        g, dy = (ict.DevCE.from_host(CE(t.mant, (t.exp.astype(int) + k).astype(np.int8), 1, G)) for t, k in ((gamma, up), (dY, s - up)))
+        got = ict.layernorm_bwd(x, g, dy, (0, 0), g_out)[0].to_host()
+        k = np.where(ref.exp == E_ZERO, 0, ref.exp.astype(int) + s - 127)
+        assert np.array_equal(got.exp, np.where(ref.exp == E_ZERO, E_ZERO, np.minimum(ref.exp.astype(int) + s, 127))), s
+        kk = np.repeat(k, g_out, 1)
+        assert np.array_equal(got.mant[kk <= 0], ref.mant[kk <= 0]), s
+        over = (kk > 0) & ((np.abs(ref.mant) - 0.5) * np.exp2(np.clip(kk, 0, 60)) >= 127.5)
+        assert over.any() == (s > 127 - top) and np.array_equal(got.mant[over], 127 * np.sign(ref.mant[over])), s
+        code, _ = ict.ict_get_device_status()
+        assert (code != 0) == (s > 127 - top)
