@@ -94,19 +94,30 @@ struct NormArgs {
     int ngx, ngd, ngg, ngb, ngo;    // groups per row
     int fast, gso;                  // an output group is a power of two of neighbouring lanes, its log2
     int eps_mul, eps_shift;
-    float4 *stat;                   // backward: {S1, R, row exponent, 0} of every row
+    float4 *stat;                   // backward: {S1, R 2^down, row exponent, 0} of every row
     int32_t *col_top;               // backward: largest exponent of dY's column groups + 256 (0: all zero)
 };
 
-// (R, h's multiplier) of a row: D is formed exactly, then rounded to 24 bits, its root
-// and the reciprocal each again to 24 bits.
-__device__ __forceinline__ float row_scale(const NormArgs &p, int s1, int s2, int e) {
-    int64_t D = (int64_t)p.N * s2 - (int64_t)s1 * s1;
+// R 2^down of a row: D is formed exactly, then rounded to 24 bits, its root and the reciprocal each
+// again to 24 bits.  Rows of small values have an eps term of up to 2^290 in their units: from 2^62
+// on it is brought down by an even power of two, 2^(2 down), to between 2^60 and 2^62, where the bits of
+// the rest that fall off count as one (they lie far below the 24 bits).  There |u R 2^8| <=
+// 2^21 2^-30 2^8 rounds to h = 0, so down matters to dX alone.
+__device__ __forceinline__ float row_scale(const NormArgs &p, int s1, int s2, int e, int &down) {
+    int64_t D = (int64_t)p.N * s2 - (int64_t)s1 * s1;  // below 2^41
+    down = 0;
     if (e > kNoExp && p.eps_mul) {
-        const int64_t m = (int64_t)p.eps_mul * p.N * p.N;  // below 2^36
+        const int64_t m = (int64_t)p.eps_mul * p.N * p.N;  // 2^8 to 2^35
         const int k = -p.eps_shift - 2 * e;
-        const int64_t cap = 1ll << 60;
-        D += k >= 0 ? ((k > 60 || m > (cap >> k)) ? cap : m << k) : (k < -62 ? 0 : m >> -k);
+        if (k >= 0) {
+            down = max(0, 64 - __clzll(m) + k - 61) >> 1;
+            const int j = 2 * down, jd = min(j, 62);
+            const int64_t lost = D & ((1ll << jd) - 1);
+            D = (m << (k - j)) + (D >> jd);
+            D |= lost != 0;
+        } else {
+            D += k < -62 ? 0 : m >> -k;
+        }
     }
     return D > 0 ? __frcp_rn(__fsqrt_rn(__ll2float_rn(D))) : 0.0f;
 }
@@ -184,7 +195,7 @@ __device__ __forceinline__ uint4 fit16(const f2 (&y)[8], uint32_t top, int base,
     }
     const int need = need_rel_f32(top, 8) + base;
     e = finalize_exp(need);
-    // a capped exponent lies up to 250 below base; every y is 0 or at least 2^-26, so 2^127 saturates as well
+    // a capped exponent lies up to 250 below base; every y is 0 or at least 2^-27, so 2^127 saturates as well
     const f2 sc = pk(pow2f(min(base - e, 127))), mg = pk(kMagic);
     uint32_t o[4];
 #pragma unroll
@@ -360,7 +371,8 @@ __global__ void __launch_bounds__(256, 3) norm_fwd_kernel(const __grid_constant_
             }
         }
         lanes_all<L>(s12, red, Sum());
-        const f2 N2 = pk((float)p.N), m1 = pk(-(float)s1), R2 = pk(row_scale(p, s1, s2, e) * 256.0f);
+        int down;
+        const f2 N2 = pk((float)p.N), m1 = pk(-(float)s1), R2 = pk(row_scale(p, s1, s2, e, down) * 256.0f);
         const f2 mg = pk(kMagic), nmg = pk(-kMagic);
         fit_row<L, V>(p, row, live, lr, eb, gm, [&](int v, f2(&y)[8]) {
             const uint32_t u[4] = {w[v].x ^ 0x80808080u, w[v].y ^ 0x80808080u, w[v].z ^ 0x80808080u,
@@ -460,7 +472,8 @@ __global__ void __launch_bounds__(256, 2) norm_bwd_kernel(const __grid_constant_
             }
         }
         lanes_all<L>(s12, red, Sum());
-        const float R = row_scale(p, s1, s2, e);
+        int down;
+        const float R = row_scale(p, s1, s2, e, down);
         if (live && lr == 0) p.stat[row] = make_float4((float)s1, R, __int_as_float(e), 0.0f);
         const f2 N2 = pk((float)p.N), ms = pk(-(float)s1), R2 = pk(R * 256.0f), mg = pk(kMagic), nmg = pk(-kMagic);
         // S3 = sum g and S4 = sum g h: g in 16-bit halves, h in its two bytes
@@ -496,7 +509,7 @@ __global__ void __launch_bounds__(256, 2) norm_bwd_kernel(const __grid_constant_
         const f2 m1 = pk(-(float)rint(mean(4.0 * (double)s3)));
         const f2 m2 = pk((float)mean((double)s4) * 6.103515625e-05f);  // 2^-14
         const f2 RN = pk(R * (float)p.N), four = pk(4.0f), one = pk(-1.0f);
-        const int base = (e <= kNoExp ? 0 : eg + (e2 <= kNoExp ? 0 : e2) - e - 2);
+        const int base = (e <= kNoExp ? 0 : eg + (e2 <= kNoExp ? 0 : e2) - e - 2) - down;
         fit_row<L, V>(p, row, live, lr, base, gm, [&](int v, f2(&y)[8]) {
             const int q = min(v * L + lr, p.nvec - 1);
             const uint32_t u[4] = {w[v].x ^ 0x80808080u, w[v].y ^ 0x80808080u, w[v].z ^ 0x80808080u,

@@ -3,10 +3,12 @@
 Plain numpy on whole numbers (int64), written from the definitions in include/ict.h one
 sequence and one head at a time.  Rounding is half to even throughout.  A number that the
 definition rounds to 24 significant bits is a numpy float32, whose conversion, division and
-square root round correctly; everything else is an int64 with a power of two beside it.
+square root round correctly, or a Fraction where its exponent has no bound; everything else is
+an int64 with a power of two beside it.
 """
 from __future__ import annotations
 
+import math
 from fractions import Fraction
 
 import numpy as np
@@ -87,6 +89,25 @@ def store(out: CE, row, col, nums, den, r):
 
 # ------------------------------------------------------------------ layer norm
 
+def _rn24(x: Fraction) -> Fraction:
+    if x == 0:
+        return x
+    k = bitlen(abs(x.numerator)) - bitlen(x.denominator) - 25
+    while abs(x) / Fraction(2) ** k >= 2 ** 24:
+        k += 1
+    return round(x / Fraction(2) ** k) * Fraction(2) ** k
+
+
+def _rn24_sqrt(d: Fraction) -> Fraction:
+    """rn24 of the root of a number of 24 bits and any exponent: the whole root of it times 2^60, with a half behind
+    where digits follow."""
+    k = bitlen(d.numerator) - bitlen(d.denominator) & ~1
+    m = d / Fraction(2) ** k * 2 ** 60
+    assert m.denominator == 1
+    r = math.isqrt(int(m))
+    return _rn24(Fraction(2 * r + (r * r != m), 2 ** 31)) * Fraction(2) ** (k // 2)
+
+
 def _row_norm(C, e, eps):
     """h (at 2^-8), R and the row's exponent."""
     a, top = align(C, e)
@@ -96,25 +117,16 @@ def _row_norm(C, e, eps):
     if top is not None:
         k = -eps[1] - 2 * top
         add = eps[0] * N * N
-        D += min(add << k if k >= 0 else add >> -k, 1 << 60)
-    R = np.float32(1) / np.sqrt(np.float32(np.int64(D))) if D > 0 else np.float32(0)
-    m, k = parts(R)
-    return rne_shift((N * a - s1) * m, -(k + 8)), R, top
+        D += add << k if k >= 0 else add >> -k
+    R = _rn24(1 / _rn24_sqrt(_rn24(Fraction(D)))) if D > 0 else Fraction(0)
+    k = bitlen(R.denominator) - 1
+    return rne_shift((N * a - s1) * R.numerator, k - 8), R, top
 
 
 def _vector(t: CE, base):
     e = exps(t)[0]
     keep = (e != E_ZERO) & (e >= base - 100)
     return np.where(keep, t.mant[0].astype(np.int64), 0), np.where(keep, e, base)
-
-
-def _rn24(x: Fraction) -> Fraction:
-    if x == 0:
-        return x
-    k = bitlen(abs(x.numerator)) - bitlen(x.denominator) - 25
-    while abs(x) / Fraction(2) ** k >= 2 ** 24:
-        k += 1
-    return round(x / Fraction(2) ** k) * Fraction(2) ** k
 
 
 def _fit_fractions(out: CE, row, vals, r):
@@ -158,7 +170,7 @@ def layernorm_bwd(X: CE, gamma: CE, dY: CE, eps=(1, 20), g_cols=32):
         m1 = _mant(4 * s3, N, 0)
         m2, k2 = parts(np.float32(np.float64(s4) / np.float64(N)))
         t = 4 * g - m1 - rne_shift(h * m2, 14 - k2)
-        RN = Fraction(float(R * np.float32(N)))
+        RN = _rn24(R * N)
         if top is None:
             continue  # a row of zeros: R = 0 unless another row's, nothing passes
         _fit_fractions(dX, i, [_rn24(int(v) * RN) for v in t], (top_g or 0) + (top_d or 0) - top - 2)

@@ -197,3 +197,20 @@ def test_layernorm_gradients_beyond_the_largest_exponent(ict, G, g_out):
         assert over.any() == (s > 127 - top) and np.array_equal(got.mant[over], 127 * np.sign(ref.mant[over])), s
         code, _ = ict.ict_get_device_status()
         assert (code != 0) == (s > 127 - top)
+
+
+@pytest.mark.parametrize("N,G,g_out", [(16, 16, 16), (64, 32, 32), (208, 16, 48), (768, 64, 32), (2064, 48, 16), (8192, 64, 128)])
+def test_layernorm_of_small_rows(ict, N, G, g_out):
+    """Rows of every exponent down to -127, where the eps term in the row's units grows from nothing to 2^290."""
+    rng = np.random.default_rng(N)
+    es = list(range(-127, -18)) if N < 1000 else [-127, -126, -90, -60, -51, -50, -41, -40, -33, -32, -31, -30, -29, -28, -27, -26, -20]
+    X, dY = rand_ce(rng, len(es), N, 1, G, elo=0, ehi=0, zero_groups=0.1), rand_ce(rng, len(es), N, 1, G, elo=-17, ehi=-15)
+    X.exp = np.where(X.exp == E_ZERO, E_ZERO, np.array(es)[:, None]).astype(np.int8)
+    gamma = rand_ce(rng, 1, N, 1, 16, elo=-7, ehi=-6)
+    x, dy, g = (ict.DevCE.from_host(t) for t in (X, dY, gamma))
+    for eps in ((1, 20), (512, 0), (7, 64)):
+        same(ict.layernorm_fwd(x, g, None, eps, g_out).to_host(), blocks.layernorm_fwd(X, gamma, None, eps, g_out), f"Y {eps}")
+        ref = blocks.layernorm_bwd(X, gamma, dY, eps, g_out)
+        for name, t, r in zip(("dX", "dgamma", "dbeta"), ict.layernorm_bwd(x, g, dy, eps, g_out), ref):
+            same(t.to_host(), r, f"{name} {eps}")
+    status_ok(ict)
