@@ -407,7 +407,8 @@ int32_t ict_softmax_ce(const ict_tensor *Z, const int32_t *target, int32_t *loss
 /* the pages print no formula for an integer layer norm, so this is a reading).          */
 /*   a = ALIGN_MAX(row of X), e its exponent; S1 = sum a; S2 = sum a^2; u = N a - S1;     */
 /*   D = N S2 - S1^2 + floor(eps_mul N^2 2^(-eps_shift - 2 e))  (eps in X's units as a     */
-/*       multiply-shift; no eps term for a row of zeros);                                  */
+/*       multiply-shift; e = ICT_E_ZERO = -128 for a row of zeros, whose gradient is that of */
+/*       a very small row, (g - mean g) / sqrt(eps): rows that only pad want a dY of zeros);  */
 /*   R = rn24(1 / rn24(sqrt(rn24(D)))), rn24 = rounded to 24 significant bits at any        */
 /*       exponent, R = 0 when D = 0;                                                        */
 /*   h = RNE(u R 2^8): the normalised row as a 16-bit integer at 2^-8.                      */

@@ -98,17 +98,20 @@ struct NormArgs {
     int32_t *col_top;               // backward: largest exponent of dY's column groups + 256 (0: all zero)
 };
 
+// a row of zeros counts as the smallest there is: its gradient is that of small rows, (g - mean g) / sqrt(eps)
+__device__ __forceinline__ int row_exponent(int e) { return e <= kNoExp ? kEZero : e; }
+
 // R 2^down of a row: D is formed exactly, then rounded to 24 bits, its root and the reciprocal each
-// again to 24 bits.  Rows of small values have an eps term of up to 2^290 in their units: from 2^62
+// again to 24 bits.  Rows of small values have an eps term of up to 2^292 in their units: from 2^62
 // on it is brought down by an even power of two, 2^(2 down), to between 2^60 and 2^62, where the bits of
 // the rest that fall off count as one (they lie far below the 24 bits).  There |u R 2^8| <=
 // 2^21 2^-30 2^8 rounds to h = 0, so down matters to dX alone.
 __device__ __forceinline__ float row_scale(const NormArgs &p, int s1, int s2, int e, int &down) {
     int64_t D = (int64_t)p.N * s2 - (int64_t)s1 * s1;  // below 2^41
     down = 0;
-    if (e > kNoExp && p.eps_mul) {
+    if (p.eps_mul) {
         const int64_t m = (int64_t)p.eps_mul * p.N * p.N;  // 2^8 to 2^35
-        const int k = -p.eps_shift - 2 * e;
+        const int k = -p.eps_shift - 2 * row_exponent(e);
         if (k >= 0) {
             down = max(0, 64 - __clzll(m) + k - 61) >> 1;
             const int j = 2 * down, jd = min(j, 62);
@@ -509,7 +512,7 @@ __global__ void __launch_bounds__(256, 2) norm_bwd_kernel(const __grid_constant_
         const f2 m1 = pk(-(float)rint(mean(4.0 * (double)s3)));
         const f2 m2 = pk((float)mean((double)s4) * 6.103515625e-05f);  // 2^-14
         const f2 RN = pk(R * (float)p.N), four = pk(4.0f), one = pk(-1.0f);
-        const int base = (e <= kNoExp ? 0 : eg + (e2 <= kNoExp ? 0 : e2) - e - 2) - down;
+        const int base = eg + (e2 <= kNoExp ? 0 : e2) - row_exponent(e) - 2 - down;
         fit_row<L, V>(p, row, live, lr, base, gm, [&](int v, f2(&y)[8]) {
             const int q = min(v * L + lr, p.nvec - 1);
             const uint32_t u[4] = {w[v].x ^ 0x80808080u, w[v].y ^ 0x80808080u, w[v].z ^ 0x80808080u,

@@ -109,15 +109,15 @@ def _rn24_sqrt(d: Fraction) -> Fraction:
 
 
 def _row_norm(C, e, eps):
-    """h (at 2^-8), R and the row's exponent."""
+    """h (at 2^-8), R and the row's exponent (E_ZERO for a row of zeros)."""
     a, top = align(C, e)
+    top = E_ZERO if top is None else top
     N = len(a)
     s1, s2 = int(a.sum()), int((a * a).sum())
     D = N * s2 - s1 * s1
-    if top is not None:
-        k = -eps[1] - 2 * top
-        add = eps[0] * N * N
-        D += add << k if k >= 0 else add >> -k
+    k = -eps[1] - 2 * top
+    add = eps[0] * N * N
+    D += add << k if k >= 0 else add >> -k
     R = _rn24(1 / _rn24_sqrt(_rn24(Fraction(D)))) if D > 0 else Fraction(0)
     k = bitlen(R.denominator) - 1
     return rne_shift((N * a - s1) * R.numerator, k - 8), R, top
@@ -171,8 +171,6 @@ def layernorm_bwd(X: CE, gamma: CE, dY: CE, eps=(1, 20), g_cols=32):
         m2, k2 = parts(np.float32(np.float64(s4) / np.float64(N)))
         t = 4 * g - m1 - rne_shift(h * m2, 14 - k2)
         RN = _rn24(R * N)
-        if top is None:
-            continue  # a row of zeros: R = 0 unless another row's, nothing passes
         _fit_fractions(dX, i, [_rn24(int(v) * RN) for v in t], (top_g or 0) + (top_d or 0) - top - 2)
     sums, bsum, r = np.zeros(N, object), np.zeros(N, object), np.zeros(N, np.int64)
     for j in range(0, N, dY.g_cols):

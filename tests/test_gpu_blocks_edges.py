@@ -214,3 +214,18 @@ def test_layernorm_of_small_rows(ict, N, G, g_out):
         for name, t, r in zip(("dX", "dgamma", "dbeta"), ict.layernorm_bwd(x, g, dy, eps, g_out), ref):
             same(t.to_host(), r, f"{name} {eps}")
     status_ok(ict)
+
+
+@pytest.mark.parametrize("rows,N,G,g_out", [(1, 16, 16, 16), (9, 192, 32, 32), (5, 80, 16, 80), (3, 1600, 64, 32), (2, 8192, 64, 64)])
+def test_layernorm_of_zero_rows(ict, rows, N, G, g_out):
+    """Rows of zeros alone, and among others."""
+    rng = np.random.default_rng(rows)
+    X, dY, gamma = (rand_ce(rng, r, N, 1, G, elo=e, ehi=e + 2) for r, e in ((rows, -6), (rows, -17), (1, -7)))
+    for zero in (slice(0, 1), slice(rows - 1, rows), slice(0, rows)):
+        X.mant[zero], X.exp[zero] = 0, E_ZERO
+        for eps in ((1, 20), (0, 0), (512, 64)):
+            ref = blocks.layernorm_bwd(X, gamma, dY, eps, g_out)
+            got = ict.layernorm_bwd(*(ict.DevCE.from_host(t) for t in (X, gamma, dY)), eps, g_out)
+            for name, t, r in zip(("dX", "dgamma", "dbeta"), got, ref):
+                same(t.to_host(), r, f"{name} {eps}")
+    status_ok(ict)

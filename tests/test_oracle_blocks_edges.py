@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from integer_only_nn_02_b200.workloads import CE, E_ZERO
 from oracle import blocks
 from tests.test_oracle_blocks import quantise, values
 
@@ -35,3 +36,21 @@ def test_layernorm_gradient_of_small_rows(N, eps):
     tol = np.abs(ref).max(1, keepdims=True) / 128 * 1.01 + slack
     assert (np.abs(dX - ref) <= tol).all(), (np.abs(dX - ref) / tol).max(1)
     assert (np.linalg.norm(dX, axis=1) < 1.1 * np.linalg.norm(ref, axis=1)).all()
+
+
+@pytest.mark.parametrize("eps", [(1, 20), (512, 0), (1, 64)])
+def test_layernorm_gradient_of_zero_rows(eps):
+    """A row of zeros is the limit of small rows: (g - mean g) / sqrt(eps).  t is off by at most half a unit (m1), an
+    eighth of g's; R by three roundings to 24 bits; FIT by half a step."""
+    rng = np.random.default_rng(3)
+    N = 192
+    X = CE(np.zeros((4, N), np.int8), np.full((4, N // 32), E_ZERO, np.int8), 1, 32)
+    gamma, dY = quantise(1 + 0.2 * rng.standard_normal((1, N)), N), quantise(rng.standard_normal((4, N)) * 1e-3, N)
+    dY.mant[3], dY.exp[3] = 0, E_ZERO
+    dX, dg, db = (values(t) for t in blocks.layernorm_bwd(X, gamma, dY, eps, 32))
+    ref, _, _, inv = layernorm_gradient(values(X), values(gamma)[0], values(dY), eps[0] * 2.0 ** -eps[1])
+    unit = np.exp2(blocks.exps(dY)[:3].astype(float) + blocks.exps(gamma).astype(float))
+    tol = np.abs(ref[:3]).max(1, keepdims=True) / 128 * 1.01 + unit / 8 * 1.01 * inv[:3]
+    assert (np.abs(dX[:3] - ref[:3]) <= tol).all() and not dX[3].any()
+    assert not dg.any() and db.any()
+    assert not values(blocks.layernorm_bwd(X, gamma, dY, (0, 0), 32)[0]).any()
