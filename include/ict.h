@@ -454,9 +454,9 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
 /*   d = clamp(RNE(sum_d AdO AO 2^(eO - eV)), +-(2^22 - 1)), AO a row of one head aligned;     */
 /*   x = AdO AV^T - d;  X = 127 sum_d |AdO| + |d|;  t = bitlen(X);  T = RNE(E x 2^-t);         */
 /*   dQ = FIT(scale_mul sum_j T AK 2^(-scale_shift + t + edO + eV + eK) / S);                  */
-/*   per block of 128 keys, over the queries that see any of it (all query heads of the       */
-/*   key/value head): p = bitlen(min S) - 1, r = rn24(2^p / rn24(S)), c = max(0, bitlen(max of  */
-/*   floor(r (max_j |T| + 1) 2^t) + X) - 14);  P = RNE(E r);  U = RNE(P x 2^-c);               */
+/*   per block of 128 keys, over the queries that see any of it and have X > 0 (all query heads */
+/*   of the key/value head): p = bitlen(min S) - 1, r = rn24(2^p / rn24(S)), c = max(0,         */
+/*   bitlen(max of floor(r (max_j |T| + 1) 2^t) + X) - 14);  P = RNE(E r);  U = RNE(P x 2^-c);  */
 /*   dV = FIT(sum P AdO 2^(edO - p));  dK = FIT(scale_mul sum U AQ 2^(c - p - scale_shift +     */
 /*   edO + eV + eQ)).                                                                          */
 /* head_dim a multiple of 16 up to 128, heads_q <= 256, batch heads_kv <= 65535, len_q and       */

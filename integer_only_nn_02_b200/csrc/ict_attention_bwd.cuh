@@ -427,7 +427,10 @@ __device__ __forceinline__ KeyItem key_item(const AttnArgs &a, int item) {
 }
 
 // The exponents of every key block: pi from the smallest sum of weights, c from the largest bound,
-// over the queries that see the block; those of the accumulators of dV and dK.  One block of threads each, of up to 1024.
+// over the queries that see the block and have a gradient; those of the accumulators of dV and dK.  One block of threads
+// each, of up to 1024.  A query with X = 0 (dO aligned to zeros, and with it every x) adds nothing to dV and dK whatever
+// its P is, and P that pass 16 bits there do no harm; counted, one such query with all its weight on one key would
+// leave flat queries over 65536 keys no digit.
 __global__ void __launch_bounds__(1024) attn_exps_kernel(const __grid_constant__ AttnArgs a) {
     __shared__ int smin;
     __shared__ unsigned long long bmax;
@@ -444,8 +447,9 @@ __global__ void __launch_bounds__(1024) attn_exps_kernel(const __grid_constant__
     int m = INT_MAX;
 #pragma unroll 4
     for (int t = threadIdx.x; t < total; t += blockDim.x) {
-        const int S = a.stats[row(t)].y;
-        m = S > 0 ? min(m, S) : m;
+        const int64_t at = row(t);
+        const int S = a.stats[at].y;
+        m = S > 0 && a.row[at].y > 0 ? min(m, S) : m;
     }
     m = -warp_max(-m);
     if ((threadIdx.x & 31) == 0) atomicMin(&smin, m);
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(1024) attn_exps_kernel(const __grid_constant__
     for (int t = threadIdx.x; t < total; t += blockDim.x) {
         const int64_t at = row(t);
         const int S = a.stats[at].y, tmax = a.tmax[at], X = a.row[at].y;
-        if (S > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), tmax, X));
+        if (S > 0 && X > 0) x = max(x, (unsigned long long)attn_bound(attn_rho(S, pi), tmax, X));
     }
     for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
     if ((threadIdx.x & 31) == 0) atomicMax(&bmax, x);

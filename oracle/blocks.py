@@ -292,11 +292,15 @@ def attention_bwd(d, Q: CE, K: CE, V: CE, O: CE, dO: CE, lens_q=None, lens_k=Non
                 rows = H.vis[:, js].any(1)
                 if not rows.any():
                     continue
-                p = bitlen(min(int(S[rows].min()) for _, S, _, _, _ in per)) - 1
+                # queries without a gradient add nothing and choose no exponent
+                sums = [int(s) for _, S, _, X, _ in per for s in S[rows & (X > 0)]]
+                if not sums:
+                    continue
+                p = bitlen(min(sums)) - 1
                 rho = [np.float32(2.0 ** p) / np.maximum(S, 1).astype(np.float32) for _, S, _, _, _ in per]
                 bound = 0
                 for (E, S, x, X, tm), rr in zip(per, rho):
-                    for i in np.flatnonzero(rows):
+                    for i in np.flatnonzero(rows & (X > 0)):
                         mm, kk = parts(rr[i])
                         v = mm * (int(tm[i]) + 1)
                         k = kk + bitlen(X[i])
@@ -304,7 +308,7 @@ def attention_bwd(d, Q: CE, K: CE, V: CE, O: CE, dO: CE, lens_q=None, lens_k=Non
                 c = max(0, bitlen(bound) - 14)
                 sv, sk = np.zeros((js.stop - j, D), np.int64), np.zeros((js.stop - j, D), np.int64)
                 for r, ((E, S, x, X, tm), rr) in enumerate(zip(per, rho)):
-                    for i in np.flatnonzero(rows):
+                    for i in np.flatnonzero(rows & (X > 0)):
                         mm, kk = parts(rr[i])
                         P = rne_shift(E[i, js] * mm, -kk)
                         U = rne_shift(P * x[i, js], c)

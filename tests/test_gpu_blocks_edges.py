@@ -229,3 +229,25 @@ def test_layernorm_of_zero_rows(ict, rows, N, G, g_out):
             for name, t, r in zip(("dX", "dgamma", "dbeta"), got, ref):
                 same(t.to_host(), r, f"{name} {eps}")
     status_ok(ict)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Lq,Lk,D,G,causal", [(1, 1, 64, 3000, 32, 32, False), (4, 2, 40, 300, 64, 64, True),
+                                                     (2, 1, 30, 700, 128, 32, False), (8, 1, 150, 260, 64, 16, True)])
+def test_attention_backward_of_queries_without_a_gradient(ict, Hq, Hkv, Lq, Lk, D, G, causal):
+    """Peaked queries whose dO is zero, among flat ones: the others' digits are their own.  And a key head of which no
+    query has a gradient."""
+    c = Case(Lk, 2, Hq, Hkv, Lq, Lk, D, causal, G=G, elo=-8, ehi=-8, zero=0.0)
+    c.Q.mant = (c.Q.mant // 8).astype(np.int8)
+    for i in (3, 17):
+        for b in range(2):
+            c.Q.mant[b * Lq + i] = np.sign(c.Q.mant[b * Lq + i]) * 127
+            c.K.mant[b * Lk + 2, : Hkv * D] = np.tile(np.sign(c.Q.mant[b * Lq + 3, :D]) * 127, Hkv)
+            c.dO.mant[b * Lq + i], c.dO.exp[b * Lq + i] = 0, E_ZERO
+    c.Q.exp[:] = c.K.exp[:] = -5
+    c.check(ict, G)
+    if Hkv > 1:
+        half = Hq // Hkv * D
+        c.dO.mant[:, :half], c.dO.exp[:, : half // G] = 0, E_ZERO
+        c.check(ict, G)
+    c.dO.mant[:], c.dO.exp[:] = 0, E_ZERO
+    c.check(ict, G)
