@@ -18,7 +18,7 @@ import os
 import numpy as np
 import torch
 
-from .workloads import CE, cdiv
+from .workloads import CE, E_ZERO, cdiv
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libict.so")
@@ -688,7 +688,7 @@ def attention_fwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, g_cols=32, lens_q=None,
 def attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, O: DevCE, dO: DevCE, stats: torch.Tensor, g_cols=32,
                   lens_q=None, lens_k=None, stream=None):
     """(dQ, dK, dV) in (1, g_cols) groups, laid out like Q, K and V: operands that are different columns of one
-    tensor share their gradient's tensor (columns of no head stay unwritten)."""
+    tensor share their gradient's tensor (columns of no head are zero)."""
     made = []  # (operand, gradient, first columns and ends taken)
 
     def like(t: DevCE, first: int, heads: int) -> DevCE:
@@ -703,6 +703,10 @@ def attention_bwd(d: dict, Q: DevCE, K: DevCE, V: DevCE, O: DevCE, dO: DevCE, st
     c = attn_desc(d)
     with _on(stream):
         dQ, dK, dV = like(Q, c.q_col, c.heads_q), like(K, c.k_col, c.heads_kv), like(V, c.v_col, c.heads_kv)
+        for _, out, taken in made:
+            if sum(b - a for a, b in taken) < out.cols:  # the call writes the heads' columns alone
+                out.mant.zero_()
+                out.exp.fill_(E_ZERO)
         ict_attention_bwd(c, Q, K, V, lens_q, lens_k, O, dO, stats, dQ, dK, dV,
                           Q.mant.new_empty(ict_attention_workspace(True, c)))
     return dQ, dK, dV

@@ -251,3 +251,32 @@ def test_attention_backward_of_queries_without_a_gradient(ict, Hq, Hkv, Lq, Lk, 
         c.check(ict, G)
     c.dO.mant[:], c.dO.exp[:] = 0, E_ZERO
     c.check(ict, G)
+
+
+@pytest.mark.parametrize("packed,extra,Hq,Hkv", [(True, 4, 2, 2), (False, 2, 2, 2), (False, 0, 4, 2), (True, 0, 2, 1)])
+def test_columns_of_no_head_are_zero(ict, monkeypatch, packed, extra, Hq, Hkv):
+    """A gradient as wide as its operand is whole: what belongs to no head is zero, ready for the next product."""
+    near = ict.DevCE.near
+
+    def dirty(*a):
+        t = near(*a)
+        t.mant.fill_(77)
+        t.exp.fill_(55)
+        return t
+
+    c = Case(9, 2, Hq, Hkv, 33, 33, 32, True, packed=packed, G=16, extra=extra)
+    if not extra:
+        c.K = c.V = c.Q  # the heads of K and V are some of Q's columns
+        c.d.update(q_col=0, k_col=0, v_col=0)
+    o, _ = blocks.attention_fwd(c.d, c.Q, c.K, c.V, g_cols=16)
+    ref = blocks.attention_bwd(c.d, c.Q, c.K, c.V, o, c.dO, g_cols=16)
+    monkeypatch.setattr(ict.DevCE, "near", staticmethod(dirty))
+    got = c.gpu(ict, 16)[2:]
+    for k, t in enumerate(got):
+        want = ref[k]
+        if packed and extra:  # one tensor; 4 groups each of Q, K and V behind the further columns
+            at = extra + 4
+            want = CE(sum(r.mant for r in ref), np.concatenate([ref[0].exp[:, :at], ref[1].exp[:, at: at + 4], ref[2].exp[:, at + 4:]], 1),
+                      1, 16)
+        same(t.to_host(), want, "dQ dK dV".split()[k])
+    status_ok(ict)
