@@ -52,12 +52,7 @@ struct AttnLimits {
 };
 
 // A 31-bit or wider accumulator 256 hi + lo as a float and the error scale: |value - n| <= err 2^-22.
-__device__ __forceinline__ float acc_f32(uint32_t hi, uint32_t lo, bool narrow, float &err) {
-    if (narrow) {
-        const float n = (float)((int)hi * 256 + (int)lo);
-        err = fabsf(n);
-        return n;
-    }
+__device__ __forceinline__ float acc_f32(uint32_t hi, uint32_t lo, float &err) {
     const float h = (float)(int)hi, l = (float)(int)lo;
     err = fmaf(fabsf(h), 256.0f, fabsf(l));
     return fmaf(h, 256.0f, l);
@@ -337,7 +332,7 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
             float e;
-            m = fmaxf(m, fabsf(acc_f32(hi[q], lo[q], narrow, e)));
+            m = fmaxf(m, fabsf(acc_f32(hi[q], lo[q], e)));
             w = fmaxf(w, e);
         }
         gmax[(c0 / 16 + s) * stride] = make_float2(m, w);
@@ -366,7 +361,7 @@ __device__ __forceinline__ void fit_row_tmem(const AttnArgs &a, const AttnOut &o
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
             float er;
-            n[q] = acc_f32(hi[q], lo[q], narrow, er);
+            n[q] = acc_f32(hi[q], lo[q], er);
         }
         round16(acc, seg * 16, n, f, some, den, mul, r, live, dst + seg * 16);
     }
