@@ -181,11 +181,6 @@ __global__ void __launch_bounds__(256) attn_row_kernel(const __grid_constant__ A
 
 // ------------------------------------------------------------------ host
 
-int vec_per_group(const ict_tensor *t) {
-    return t->g_cols >= t->cols ? (int)host::cdiv(t->cols, 16) : t->g_cols / 16;
-}
-int groups_per_row(const ict_tensor *t) { return (int)host::cdiv(t->cols, t->g_cols); }
-
 // an operand (or output): heads of D columns from `col` on, row-local groups of whole vectors
 int check_heads(const ict_tensor *t, int64_t rows, int col, int64_t width) {
     int st;
@@ -304,12 +299,12 @@ Scratch scratch(const AttnArgs &a, bool back) {
 }
 
 void operand(AttnOperand &o, const ict_tensor *t, int col, int heads, int L, const int32_t *lens, int8_t *copy) {
-    o.mant = t->mant, o.exp = t->exp, o.ld = t->ld, o.ngc = groups_per_row(t), o.gv = vec_per_group(t);
+    o.mant = t->mant, o.exp = t->exp, o.ld = t->ld, o.ngc = host::groups_per_row(t), o.gv = host::vec_per_group(t);
     o.gsh = (o.gv & (o.gv - 1)) == 0 ? __builtin_ctz((unsigned)o.gv) : -1;
     o.col = col, o.heads = heads, o.L = L, o.lens = lens, o.copy = copy;
 }
 void output(AttnOut &o, const ict_tensor *t, int col, int D) {
-    o.mant = t->mant, o.exp = t->exp, o.ld = t->ld, o.ngc = groups_per_row(t);
+    o.mant = t->mant, o.exp = t->exp, o.ld = t->ld, o.ngc = host::groups_per_row(t);
     o.G = (int)std::min<int64_t>(t->g_cols, t->cols), o.col = col;
     o.gcol = col / o.G, o.dg = D / o.G;
 }
@@ -525,7 +520,7 @@ int32_t ict_attention_bwd(const ict_attn_desc *d, const ict_tensor *Q, const ict
     if ((st = host::device_info(nullptr))) return st;
     uint8_t *base = (uint8_t *)ws;
     operand(a.op[OPD], dO, 0, a.Hq, a.Lq, lens_q, (int8_t *)(base + w.copy[OPD]));
-    a.o_mant = O->mant, a.o_exp = O->exp, a.o_ld = O->ld, a.o_ngc = groups_per_row(O), a.o_gv = vec_per_group(O);
+    a.o_mant = O->mant, a.o_exp = O->exp, a.o_ld = O->ld, a.o_ngc = host::groups_per_row(O), a.o_gv = host::vec_per_group(O);
     output(a.o, dQ, d->q_col, a.D);
     output(a.dk, dK, d->k_col, a.D);
     output(a.dv, dV, d->v_col, a.D);

@@ -80,36 +80,6 @@ __device__ __forceinline__ int need_quot(double q) {  // q > 0
 }
 __device__ __forceinline__ double pow2d(int k) { return __longlong_as_double((int64_t)(k + 1023) << 52); }
 
-// ---- pairs of fp32 values: one instruction works on both halves of a 64-bit register
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pk(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ f2 pk(float a) { return pk(a, a); }
-__device__ __forceinline__ void unpk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 sub2(f2 a, f2 b) {
-    f2 r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // Two weights E = RNE(2^14 2^(k / 64)), k = RNE((s - smax) f), as the floats 1.5 2^23 + E.  The
 // FMA onto 1.5 2^17 rounds the exact product once to a multiple of 2^-6; there are 960
 // arguments with a result above zero, and ex2.approx rounds to the right whole number at all

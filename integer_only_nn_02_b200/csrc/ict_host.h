@@ -20,6 +20,11 @@ int check_tensor(const ict_tensor *t);
 int check_vec(const ict_tensor *t);  // 16-byte vectors: pointer, ld, cols, group width
 int tmap_2d(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t stride, uint32_t box_inner,
             uint32_t box_outer, CUtensorMapSwizzle sw);
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+// of a tensor that check_vec has passed: groups of a row, 16-column vectors of a group
+inline int groups_per_row(const ict_tensor *t) { return (int)cdiv(t->cols, t->g_cols); }
+inline int vec_per_group(const ict_tensor *t) { return (int)((t->g_cols >= t->cols ? t->cols : t->g_cols) / 16); }
 // columns [c, c + w) of `rows` rows of bytes, ld apart
 struct Bytes {
     intptr_t at;
@@ -27,8 +32,8 @@ struct Bytes {
 };
 inline Bytes mantissas(const ict_tensor *t, int64_t c, int64_t w) { return {(intptr_t)t->mant + c, t->rows, t->ld, w}; }
 inline Bytes exponents(const ict_tensor *t, int64_t c, int64_t w) {
-    const int64_t g0 = c / t->g_cols, g1 = (c + w + t->g_cols - 1) / t->g_cols;
-    return {(intptr_t)t->exp + g0, (t->rows + t->g_rows - 1) / t->g_rows, (t->cols + t->g_cols - 1) / t->g_cols, g1 - g0};
+    const int64_t g0 = c / t->g_cols;
+    return {(intptr_t)t->exp + g0, cdiv(t->rows, t->g_rows), groups_per_row(t), cdiv(c + w, t->g_cols) - g0};
 }
 // a and b share a byte.  Rows of one ld repeat the pattern of the first two; rows of different ld whose ranges
 // meet count as shared.
@@ -75,8 +80,6 @@ private:
     void *impl;
 };
 
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
 }  // namespace host
 }  // namespace ict

@@ -26,30 +26,6 @@ namespace {
 constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
 constexpr int kMaxCols = 8192;
 
-// ---- pairs of fp32 values: one instruction works on both halves of a 64-bit register
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pk(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ f2 pk(float a) { return pk(a, a); }
-__device__ __forceinline__ void unpk(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 // the bytes b and b + 1 of w (stored with 0x80 added to every byte) as floats C
 __device__ __forceinline__ f2 bytes2(uint32_t w_biased, int b) {
     return add2(pk(__uint_as_float(__byte_perm(w_biased, 0x4B000000u, 0x7650 | b)),
@@ -750,9 +726,6 @@ __global__ void __launch_bounds__(256) values_kernel(const __grid_constant__ Val
 
 // ------------------------------------------------------------------ host
 
-int groups_per_row(const ict_tensor *t) { return (int)host::cdiv(t->cols, t->g_cols); }
-int vec_per_group(const ict_tensor *t) { return t->g_cols >= t->cols ? (int)(t->cols / 16) : t->g_cols / 16; }
-
 int check_rows(const ict_tensor *t, int64_t rows, int64_t cols) {
     int st;
     if ((st = host::check_tensor(t))) return st;
@@ -774,9 +747,9 @@ int fill(NormArgs &a, const ict_tensor *X, const ict_tensor *gamma, const ict_te
         return st;
     memset(&a, 0, sizeof(a));
     a.x = X->mant, a.x_exp = X->exp, a.ldx = X->ld, a.rows = X->rows, a.N = (int)X->cols, a.nvec = a.N / 16;
-    a.gvx = vec_per_group(X), a.ngx = groups_per_row(X);
-    a.g = gamma->mant, a.g_exp = gamma->exp, a.gvg = vec_per_group(gamma), a.ngg = groups_per_row(gamma);
-    a.out = out->mant, a.out_exp = out->exp, a.ldo = out->ld, a.gvo = vec_per_group(out), a.ngo = groups_per_row(out);
+    a.gvx = host::vec_per_group(X), a.ngx = host::groups_per_row(X);
+    a.g = gamma->mant, a.g_exp = gamma->exp, a.gvg = host::vec_per_group(gamma), a.ngg = host::groups_per_row(gamma);
+    a.out = out->mant, a.out_exp = out->exp, a.ldo = out->ld, a.gvo = host::vec_per_group(out), a.ngo = host::groups_per_row(out);
     a.eps_mul = eps_mul, a.eps_shift = eps_shift;
     return ICT_OK;
 }
@@ -861,7 +834,7 @@ int32_t ict_layernorm_fwd(const ict_tensor *X, const ict_tensor *gamma, const ic
     if ((st = fill(a, X, gamma, Y, eps_mul, eps_shift))) return st;
     if (beta) {
         if ((st = check_rows(beta, 1, X->cols))) return st;
-        a.b = beta->mant, a.b_exp = beta->exp, a.gvb = vec_per_group(beta), a.ngb = groups_per_row(beta);
+        a.b = beta->mant, a.b_exp = beta->exp, a.gvb = host::vec_per_group(beta), a.ngb = host::groups_per_row(beta);
     }
     if ((st = host::device_info(nullptr))) return st;
     if (a.rows == 0) return ICT_OK;
@@ -898,7 +871,7 @@ int32_t ict_layernorm_bwd(const ict_tensor *X, const ict_tensor *gamma, const ic
     if ((st = host::device_info(nullptr))) return st;
     cudaStream_t s = (cudaStream_t)stream;
     int64_t *acc = (int64_t *)ws;
-    a.dy = dY->mant, a.dy_exp = dY->exp, a.lddy = dY->ld, a.gvd = vec_per_group(dY), a.ngd = groups_per_row(dY);
+    a.dy = dY->mant, a.dy_exp = dY->exp, a.lddy = dY->ld, a.gvd = host::vec_per_group(dY), a.ngd = host::groups_per_row(dY);
     const int64_t acc_bytes = host::round_up((int64_t)a.N * 16, 256);
     const int64_t top_bytes = host::round_up(a.N / 4 + 4, 256);
     a.col_top = (int32_t *)((uint8_t *)ws + acc_bytes);
@@ -954,7 +927,7 @@ int32_t ict_values(const ict_tensor *t, int32_t bf16, void *out, int64_t ld_out,
     a.m = t->mant, a.e = t->exp, a.rows = t->rows, a.cols = t->cols, a.ld = t->ld, a.ldo = ld_out;
     a.g_rows = (int)std::min<int64_t>(t->g_rows, t->rows), a.g_cols = (int)std::min<int64_t>(t->g_cols, t->cols);
     a.gsh = (a.g_cols & (a.g_cols - 1)) == 0 ? __builtin_ctz((unsigned)a.g_cols) : -1;
-    a.ngc = groups_per_row(t);
+    a.ngc = host::groups_per_row(t);
     a.out = out;
     const bool vec = host::check_vec(t) == ICT_OK && (uintptr_t)out % 16 == 0 && ld_out % 8 == 0;
     a.wide = (uintptr_t)out % 32 == 0 && ld_out % (bf16 ? 16 : 8) == 0;
