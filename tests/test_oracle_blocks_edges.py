@@ -4,7 +4,7 @@ import pytest
 
 from integer_only_nn_02_b200.workloads import CE, E_ZERO
 from oracle import blocks
-from tests.test_oracle_blocks import quantise, values
+from tests.test_oracle_blocks import quantise, rel, smooth_case, softmax_attention, values
 
 
 def layernorm_gradient(x, g, dy, eps):
@@ -93,3 +93,39 @@ def test_gradients_beside_a_peaked_query_without_one(m):
     _, gk, gv = (values(t) for t in blocks.attention_bwd(d, Q, K, V, O, dO, g_cols=32))
     for got, want in ((gk, dK), (gv, dV)):
         assert np.linalg.norm(got - want) < 0.03 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("n,m,causal,D", [(200, 700, False, 64), (300, 300, True, 64), (40, 1500, False, 32)])
+def test_attention_follows_the_formula_at_length(n, m, causal, D):
+    """Attention and its gradients of the operands' own values.  An aligned element is off by at most half a step of a
+    grid on which the largest of all rows, below 5 (of up to 10^5 normal draws), is at least 64 steps: 5 / 128 / sqrt(3)
+    = 2.3 percent of a standard deviation.  A score, scaled by 1 / sqrt(D), sums D products with such an error in either
+    factor: 2.3 sqrt(2) = 3.2 percent, and a weight with it.  V adds 2.3 percent and FIT 0.5: 6 percent of the norm,
+    twice that as the bound; the gradients pass through two such products."""
+    d, q, k, v, do, vis = smooth_case(n + m, n, m, D, causal)
+    d["scale"] = {64: (1, 3), 32: (181, 10)}[D]
+    scale = d["scale"][0] * 2.0 ** -d["scale"][1]
+    o, _ = blocks.attention_fwd(d, q, k, v, g_cols=32)
+    Q, K, V, dO = (values(t) for t in (q, k, v, do))
+    p, ref = softmax_attention(Q, K, V, vis, scale)
+    assert rel(values(o), ref) < 0.12
+    dP = dO @ V.T
+    dS = p * (dP - (p * dP).sum(1, keepdims=True))
+    dQ, dK, dV = blocks.attention_bwd(d, q, k, v, o, do, g_cols=32)
+    for got, want in ((dQ, dS @ K * scale), (dK, dS.T @ Q * scale), (dV, p.T @ dO)):
+        assert rel(values(got), want) < 0.24
+
+
+@pytest.mark.parametrize("m", [300, 2048])
+def test_attention_of_the_aligned_operands(m):
+    """Beside the alignment, what is rounded moves outputs and gradients by 3 percent at any length (the sum of
+    test_gradients_beside_a_peaked_query_without_one)."""
+    rng = np.random.default_rng(m)
+    D, n = 64, 48
+    d = dict(batch=1, heads_q=1, heads_kv=1, len_q=n, len_k=m, head_dim=D, scale=(1, 3))
+    Q, K, V = (quantise(rng.standard_normal((r, D)), 32) for r in (n, m, m))
+    dO = quantise(rng.standard_normal((n, D)) * 1e-3, 32)
+    O, _ = blocks.attention_fwd(d, Q, K, V, g_cols=32)
+    want = aligned_attention(d, Q, K, V, O, dO)
+    for got, ref in zip((O, *blocks.attention_bwd(d, Q, K, V, O, dO, g_cols=32)), want):
+        assert rel(values(got), ref) < 0.03
