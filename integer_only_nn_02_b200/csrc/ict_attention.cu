@@ -205,6 +205,10 @@ int check_out(const ict_tensor *t, int64_t rows, int col, int64_t width, int D) 
 // one part against the chosen number: 3 x 8 causal heads of 2048 tokens on 2, 144 us against 81 us;
 // 3 causal heads of 4096, 77 against 52 us; 8 heads of 512 on one, 75 against 31 us.  Where one
 // part is chosen, two cost more: 12 heads of 1024 tokens 25 against 42 us, causal 24 against 28 us.
+// Heads of 128 columns have two kernels and about 1.6 times the time of all of these, so that the same numbers serve
+// (whole backward passes, one part, the chosen number, the best of 1 to 16): 371, 268 and 268 us; 240, 201 and 201 us;
+// 203, 131 and 129 us; with one part chosen 107 against 139 us, causal 104 against 117 us.  The count of SMs is the
+// B200's and not asked for: the workspace's size, which depends on the parts, is asked for without a device.
 int split_parts(const AttnArgs &a) {
     const double tiles = (double)host::cdiv(a.Lq, 128) * a.rep, blocks = a.blocks, sms = 148;
     // of the queries, those that a key sees on average
@@ -336,10 +340,12 @@ int align_operands(const AttnArgs &a, cudaStream_t s) {
     const int L = std::max(a.Lq, a.Lk);
     const int64_t vecs = std::max((int64_t)a.rep * a.Lq, (int64_t)a.Lk) * NV;
     const unsigned bg = (unsigned)(a.B * a.Hkv);
+    int sms = 148;
+    host::device_info(&sms);
     // Few vectors per block of threads, or enough heads to fill the SMs: one kernel.  12 heads of 64
     // columns: 512 rows 7.0 us against 6.7 us in three launches, 1024 rows 11.9 against 6.9; 192 heads:
     // 1024 rows 30 against 38 us, 2048 rows 58 against 68 us.
-    if (vecs <= kFuseVecs || (bg >= 148 && vecs <= 16 * kFuseVecs)) {
+    if (vecs <= kFuseVecs || (bg >= (unsigned)sms && vecs <= 16 * kFuseVecs)) {
         attn_align_kernel<NV><<<dim3(bg, (unsigned)a.n_op), 256, 0, s>>>(a);
         host::counted(1);
         return host::launch_status();

@@ -920,7 +920,8 @@ int32_t ict_values(const ict_tensor *t, int32_t bf16, void *out, int64_t ld_out,
     if (bf16 != 0 && bf16 != 1) return ICT_ERR_INVALID_ARG;
     if (t->rows > 0 && t->cols > 0 && (!out || ld_out < t->cols)) return ICT_ERR_INVALID_ARG;
     if ((uintptr_t)out % (bf16 ? 2 : 4)) return ICT_ERR_ALIGNMENT;
-    if ((st = host::device_info(nullptr))) return st;
+    int sms = 0;
+    if ((st = host::device_info(&sms))) return st;
     if (t->rows == 0 || t->cols == 0) return ICT_OK;
     ValuesArgs a;
     memset(&a, 0, sizeof(a));
@@ -932,7 +933,7 @@ int32_t ict_values(const ict_tensor *t, int32_t bf16, void *out, int64_t ld_out,
     const bool vec = host::check_vec(t) == ICT_OK && (uintptr_t)out % 16 == 0 && ld_out % 8 == 0;
     a.wide = (uintptr_t)out % 32 == 0 && ld_out % (bf16 ? 16 : 8) == 0;
     const int64_t n = t->rows * t->cols / (vec ? 16 : 1);
-    const unsigned grid = (unsigned)std::min<int64_t>(host::cdiv(n, 256), 148 * 8);
+    const unsigned grid = (unsigned)std::min<int64_t>(host::cdiv(n, 256), (int64_t)sms * 8);
     cudaStream_t s = (cudaStream_t)stream;
     host::Timer kt(s, ICT_KC_OTHER, (double)t->rows * t->cols * (bf16 ? 3 : 5));
     if (vec && bf16) values_kernel<true, true><<<grid, 256, 0, s>>>(a);
