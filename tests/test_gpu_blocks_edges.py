@@ -280,3 +280,65 @@ def test_columns_of_no_head_are_zero(ict, monkeypatch, packed, extra, Hq, Hkv):
                       1, 16)
         same(t.to_host(), want, "dQ dK dV".split()[k])
     status_ok(ict)
+
+
+CAPTURED = """
+import torch
+from integer_only_nn_02_b200 import ict
+torch.manual_seed(0)
+
+def rnd(rows, cols, e=-6):
+    return ict.DevCE(torch.randint(-127, 128, (rows, cols), device="cuda", dtype=torch.int8),
+                     torch.full((rows, cols // 32), e, device="cuda", dtype=torch.int8), 1, 32)
+
+x, g, dy, q, do = rnd(50, 192), rnd(1, 192), rnd(50, 192, -16), rnd(260, 192), rnd(260, 64, -16)
+d = dict(batch=2, heads_q=1, heads_kv=1, len_q=130, len_k=130, head_dim=64, scale=(1, 3), q_col=0, k_col=64, v_col=128)
+
+def step():
+    o, st = ict.attention_fwd(d, q, q, q, 32)
+    r = ict.attention_bwd(d, q, q, q, o, do, st, 32)
+    y = ict.layernorm_fwd(x, g)
+    z = ict.layernorm_bwd(x, g, dy)
+    return [st, ict.values(y)] + [t for c in (o, r[0], y, *z) for t in (c.mant, c.exp)]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+"""
+
+
+def test_first_calls_are_captured(ict):
+    """A process whose first calls of all are captured into a graph."""
+    r = subprocess.run([sys.executable, "-c", CAPTURED], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("D,scale,causal", [(64, (1, 3), False), (64, (1, 3), True), (128, (181, 11), True)])
+def test_longest_sequences(ict, D, scale, causal):
+    """65536 queries over 65536 keys, of which the last 64 have a gradient: what a call with those 64 alone gives
+    (every exponent the same, so that their alignment is)."""
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    L, n = 65536, 64
+
+    def rnd(top, e):
+        return ict.DevCE(torch.randint(-top, top + 1, (L, D), generator=gen, device="cuda", dtype=torch.int8),
+                         torch.full((L, D // 32), e, device="cuda", dtype=torch.int8), 1, 32)
+
+    last = lambda t: ict.DevCE(t.mant[L - n:].contiguous(), t.exp[L - n:].contiguous(), 1, 32)  # noqa: E731
+    q, k, v, do = rnd(20, -6), rnd(20, -6), rnd(127, -6), rnd(127, -16)
+    do.mant[: L - n], do.exp[: L - n] = 0, E_ZERO
+    d = dict(batch=1, heads_q=1, heads_kv=1, len_q=L, len_k=L, head_dim=D, scale=scale, causal=causal)
+    o, stats = ict.attention_fwd(d, q, k, v, 32)
+    dq, dk, dv = ict.attention_bwd(d, q, k, v, o, do, stats, 32)
+    d["len_q"] = n
+    o1, stats1 = ict.attention_fwd(d, last(q), k, v, 32)
+    dq1, dk1, dv1 = ict.attention_bwd(d, last(q), k, v, o1, last(do), stats1, 32)
+    assert torch.equal(stats1, stats[L - n:])
+    for t, t1 in ((last(o), o1), (last(dq), dq1), (dk, dk1), (dv, dv1)):
+        assert torch.equal(t.mant, t1.mant) and torch.equal(t.exp, t1.exp)
+    assert not dq.mant[: L - n].any() and (dq.exp[: L - n] == E_ZERO).all() and dk1.mant.any() and dv1.mant.any()
+    status_ok(ict)
