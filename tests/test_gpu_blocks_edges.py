@@ -342,3 +342,50 @@ def test_longest_sequences(ict, D, scale, causal):
         assert torch.equal(t.mant, t1.mant) and torch.equal(t.exp, t1.exp)
     assert not dq.mant[: L - n].any() and (dq.exp[: L - n] == E_ZERO).all() and dk1.mant.any() and dv1.mant.any()
     status_ok(ict)
+
+
+def rnd(gen, rows, cols, e=-6, top=127):
+    return torch.randint(-top, top + 1, (rows, cols), generator=gen, device="cuda", dtype=torch.int8), \
+        torch.full((rows, cols // 32), e, device="cuda", dtype=torch.int8)
+
+
+def test_offsets_beyond_32_bits(ict):
+    """40 sequences of 65536 keys with 16 heads of 64 columns (2.7 GB each of K and V): the last sequence's outputs and
+    gradients are those of a call with it alone, by the kernels for a few queries and for tiles."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    B, L, H, D = 40, 65536, 16, 64
+    ce = lambda t, rows=None: ict.DevCE(*(x if rows is None else x[-rows:].contiguous() for x in t), 1, 32)  # noqa: E731
+    k, v = rnd(gen, B * L, H * D), rnd(gen, B * L, H * D)
+    for n in (1, 20):
+        q, do = rnd(gen, B * n, H * D, top=20), rnd(gen, B * n, H * D, e=-16)
+        d = dict(batch=B, heads_q=H, heads_kv=H, len_q=n, len_k=L, head_dim=D, scale=(1, 3))
+        o, stats = ict.attention_fwd(d, ce(q), ce(k), ce(v), 32)
+        d1 = dict(d, batch=1)
+        o1, stats1 = ict.attention_fwd(d1, ce(q, n), ce(k, L), ce(v, L), 32)
+        assert torch.equal(o.mant[-n:], o1.mant) and torch.equal(o.exp[-n:], o1.exp) and torch.equal(stats[-n * H:], stats1)
+        assert o1.mant.any()
+    got = ict.attention_bwd(d, ce(q), ce(k), ce(v), o, ce(do), stats, 32)
+    want = ict.attention_bwd(d1, ce(q, n), ce(k, L), ce(v, L), o1, ce(do, n), stats1, 32)
+    for t, t1 in zip(got, want):
+        rows = t1.mant.shape[0]
+        assert torch.equal(t.mant[-rows:], t1.mant) and torch.equal(t.exp[-rows:], t1.exp) and t1.mant.any()
+    status_ok(ict)
+
+
+def test_layernorm_offsets_beyond_32_bits(ict):
+    """2.8 million rows of 768 values, of which the last 1000 have a gradient."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    rows, N, n = 2_800_000, 768, 1000
+    x, dy, g = rnd(gen, rows, N), rnd(gen, rows, N, e=-16), rnd(gen, 1, N)
+    dy[0][:-n], dy[1][:-n] = 0, E_ZERO
+    ce = lambda t, rows=None: ict.DevCE(*(a if rows is None else a[-rows:].contiguous() for a in t), 1, 32)  # noqa: E731
+    y, y1 = ict.layernorm_fwd(ce(x), ce(g), ce(g)), ict.layernorm_fwd(ce(x, n), ce(g), ce(g))
+    assert torch.equal(y.mant[-n:], y1.mant) and torch.equal(y.exp[-n:], y1.exp)
+    dx, dg, db = ict.layernorm_bwd(ce(x), ce(g), ce(dy))
+    for t, t1 in zip((dx, dg, db), ict.layernorm_bwd(ce(x, n), ce(g), ce(dy, n))):
+        r = t1.mant.shape[0]
+        assert torch.equal(t.mant[-r:], t1.mant) and torch.equal(t.exp[-r:], t1.exp) and t1.mant.any()
+    assert not dx.mant[:-n].any()
+    for dt in (torch.float32, torch.bfloat16):
+        assert torch.equal(ict.values(y, dt)[-n:], ict.values(y1, dt))
+    status_ok(ict)
