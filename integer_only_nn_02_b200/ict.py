@@ -158,6 +158,9 @@ class DevCE:
         assert mant.dtype == torch.int8 and exp.dtype == torch.int8 and mant.is_cuda
         if exp.device != mant.device:  # the kernels read both
             raise ValueError(f"mantissas on {mant.device}, exponents on {exp.device}")
+        if not exp.is_contiguous() or mant.shape[0] > 0 and mant.shape[-1] > 1 and mant.stride(-1) != 1:
+            # a library call gets the exponents' address alone, and one stride of the mantissas
+            raise ValueError("exponents have to be contiguous, and the mantissas of a row")
         self.mant, self.exp = mant, exp
         self.rows = int(mant.shape[0])
         self.cols = int(cols if cols is not None else mant.shape[1])

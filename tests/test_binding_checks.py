@@ -32,6 +32,9 @@ class Fake:
     def stride(self, k):
         return (self.shape[1], 1)[k]
 
+    def is_contiguous(self):
+        return True
+
 
 @pytest.mark.parametrize("exp_on", [-1, 1])
 def test_exponents_elsewhere_are_refused(ict, exp_on, monkeypatch):
@@ -44,6 +47,23 @@ def test_exponents_elsewhere_are_refused(ict, exp_on, monkeypatch):
     t.exp = exp
     with pytest.raises(ValueError):
         ict._refs(t)
+
+
+def test_strided_exponents_are_refused(ict):
+    """A view of some columns of a wider tensor: its exponents do not lie one after the other."""
+
+    class On(torch.Tensor):  # host tensors that say they are on a device
+        is_cuda = True
+
+    on = lambda *shape: torch.zeros(shape, dtype=torch.int8).as_subclass(On)  # noqa: E731
+    mant, exp = on(4, 128), on(4, 4)
+    assert ict.DevCE(mant[:, 32:64], exp[:, 1:2].contiguous(), 1, 32).ld == 128
+    for bad in ((mant[:, 32:64], exp[:, 1:2]), (on(32, 4).t(), on(4, 1)), (mant[:, ::2], exp[:, :2].contiguous())):
+        with pytest.raises(ValueError):
+            ict.DevCE(*bad, 1, 32)
+    ict.DevCE(mant[:1], exp[:1], 1, 32)
+    ict.DevCE(mant[1:3], exp[1:3], 1, 32)
+    ict.DevCE(torch.empty_strided((0, 128), (0, 0), dtype=torch.int8).as_subclass(On), exp[:0], 1, 32)
 
 
 def tensor(ict, rows, cols, mant, exp, g_cols=32, ld=None):
