@@ -155,16 +155,18 @@ class DevCE:
     int8 exponent grid [cdiv(rows, g_rows), cdiv(cols, g_cols)]."""
 
     def __init__(self, mant: torch.Tensor, exp: torch.Tensor, g_rows: int, g_cols: int, cols=None):
-        assert mant.dtype == torch.int8 and exp.dtype == torch.int8 and mant.is_cuda
-        if exp.device != mant.device:  # the kernels read both
+        dev = mant.get_device()
+        assert mant.dtype is torch.int8 and exp.dtype is torch.int8 and dev >= 0
+        if exp.get_device() != dev:  # the kernels read both
             raise ValueError(f"mantissas on {mant.device}, exponents on {exp.device}")
-        if not exp.is_contiguous() or mant.shape[0] > 0 and mant.shape[-1] > 1 and mant.stride(-1) != 1:
+        rows, width = mant.shape
+        ld, step = mant.stride()
+        if not exp.is_contiguous() or (step != 1 and rows > 0 and width > 1):
             # a library call gets the exponents' address alone, and one stride of the mantissas
             raise ValueError("exponents have to be contiguous, and the mantissas of a row")
         self.mant, self.exp = mant, exp
-        self.rows = int(mant.shape[0])
-        self.cols = int(cols if cols is not None else mant.shape[1])
-        self.ld = int(mant.stride(0)) if mant.dim() == 2 and self.rows > 1 else int(mant.shape[1])
+        self.rows, self.cols = rows, width if cols is None else int(cols)
+        self.ld = ld if rows > 1 else width
         self.g_rows, self.g_cols = int(g_rows), int(g_cols)
 
     @staticmethod

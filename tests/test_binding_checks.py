@@ -18,7 +18,7 @@ class Fake:
 
     def __init__(self, index, *shape):
         self.shape, self.index = shape, index
-        self.is_cuda, self.device = index >= 0, torch.device("cuda", index) if index >= 0 else torch.device("cpu")
+        self.device = torch.device("cuda", index) if index >= 0 else torch.device("cpu")
 
     def get_device(self):
         return self.index
@@ -26,11 +26,8 @@ class Fake:
     def data_ptr(self):
         return 1 << 20
 
-    def dim(self):
-        return len(self.shape)
-
-    def stride(self, k):
-        return (self.shape[1], 1)[k]
+    def stride(self):
+        return self.shape[1], 1
 
     def is_contiguous(self):
         return True
@@ -53,7 +50,8 @@ def test_strided_exponents_are_refused(ict):
     """A view of some columns of a wider tensor: its exponents do not lie one after the other."""
 
     class On(torch.Tensor):  # host tensors that say they are on a device
-        is_cuda = True
+        def get_device(self):
+            return 0
 
     on = lambda *shape: torch.zeros(shape, dtype=torch.int8).as_subclass(On)  # noqa: E731
     mant, exp = on(4, 128), on(4, 4)
